@@ -415,6 +415,102 @@ int tg_rmsnorm_autotune(int64_t rows, int64_t n, int *occupancy, double *us);
 int tg_rmsnorm_cache_lookup(int64_t rows, int64_t n, int *occupancy, double *us, int *hit);
 int tg_rmsnorm_tunes(int64_t *n_tunes);
 
+/* ---------------------------------------------------------------- 4-bit weights and experts */
+/*
+ * Weights of the operators below.
+ *   TG_W_BF16: bf16, [N][K] row-major (a layer's output rows x input columns);
+ *     data 16-byte aligned; scales, zeros, group and scale_dtype are ignored.
+ *   TG_W_W4: 4-bit codes of a K x N matrix in panels of 16 columns and chunks
+ *     of 128 rows: data is u32 [ceil(N/16)][ceil(K/128)][64][4], 16-byte
+ *     aligned.  Word (p, c, l, t) holds column 16 p + l % 16 and rows
+ *     128 c + 32 t + 8 (l / 16) + r, r = 0..7, of which nibbles 0..3 (from
+ *     the least significant) are r = 0, 2, 4, 6 and nibbles 4..7 are
+ *     r = 1, 3, 5, 7.  scales: fp32 or bf16 (scale_dtype = TG_F32 or TG_BF16),
+ *     zeros: bytes or NULL (all 8), both [ceil(N/16)][ceil(K/group)][16].
+ *     group: 32, 64 or a multiple of 128 rows share a scale; a group may reach
+ *     past K.  Element (k, n) = scale * (code - zero).  Codes past K or N are
+ *     not used.
+ * A stack of matrices is stored one after the other.
+ */
+typedef enum { TG_W_BF16 = 0, TG_W_W4 = 1 } tg_weight_format;
+typedef struct {
+    int32_t format, group, scale_dtype, reserved;
+    const void *data, *scales, *zeros;
+} tg_weight;
+
+typedef enum {
+    TG_GATE_SILU = 0,    /* g / (1 + exp(-g)) */
+    TG_GATE_GELU = 1     /* 0.5 g (1 + erf(g / sqrt 2)) */
+} tg_gate;
+
+/*
+ * Quantises `count` K x N matrices to TG_W_W4.  W: fp32 or bf16 (dtype =
+ * TG_F32 or TG_BF16), each matrix [K][N] if rows_first, else [N][K]; words,
+ * scales and zeros as above for each; zeros NULL: symmetric codes.  values
+ * (may be NULL): what the codes stand for, in W's order and type.
+ *   symmetric:  scale = round(max |w| / 7) over the group, zero point 8
+ *   zeros:      lo = min(w, 0), hi = max(w, 0), scale = round((hi - lo) / 15),
+ *               zero = clamp(rint(-lo / scale), 0, 15)
+ *   code        = clamp(rint(w / scale) + zero, 0, 15)
+ * round is to fp32, then to scale_dtype; rint of the exact quotient, ties to
+ * even.  A group whose scale is zero has codes that stand for zero; one that
+ * holds an infinity or NaN, or whose range overflows fp32, has values that
+ * are NaN.  Storage past K and N is written as zero.  Asynchronous on the
+ * stream of tg_set_stream, as are all functions of this section; none of
+ * them allocates, so each may be captured into a graph.
+ * Limits: K, N <= 2^21, count <= 65535 (TG_E_UNSUPPORTED).
+ */
+int tg_w4_quantize(int64_t count, int64_t K, int64_t N, int group, const void *W, int dtype, int rows_first,
+                   int scale_dtype, void *words, void *scales, void *zeros, void *values);
+
+/*
+ * C = act(A . B + bias), B in 4 bits (TG_W_W4): A bf16 M x K, C M x N bf16 or
+ * fp32 (dtype = TG_BF16 or TG_BF16_F32OUT), both row-major, element alignment;
+ * bias N floats or NULL; act a tg_act.  K >= 1.  Sums are fp32; the weights'
+ * values enter the sums unrounded.  C must not overlap the inputs.  A row of A
+ * that holds an infinity gives NaN.
+ * Limits: K, N <= 2^21, M <= 2^20 (TG_E_UNSUPPORTED).
+ */
+int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void *A, const tg_weight *B, const float *bias, void *C,
+               int dtype, int act);
+
+/*
+ * Routing: for each of T tokens the k experts with the largest logits, in
+ * falling order, ties to the lowest index (a NaN counts as the largest).
+ * logits: fp32 or bf16 (dtype) T x E.  weights (T x k, fp32): softmax over all
+ * E logits, divided by the sum of the k chosen if renorm.  A row of only -inf
+ * gets experts 0..k-1 and weights 0; a row that holds +inf or NaN gets weights
+ * NaN; expert numbers are in [0, E) always.
+ * Limits: E <= 1024, k <= 16, T <= 2^24 (TG_E_UNSUPPORTED).
+ */
+int tg_moe_route(int64_t T, int64_t E, int k, const void *logits, int dtype, int renorm, int32_t *ids,
+                 float *weights);
+
+/*
+ * The experts of a gated feed-forward layer for a few tokens:
+ *   y[t] = sum_j weights[t][j] * Down_e (gate(Gate_e x[t]) * (Up_e x[t])), e = ids[t][j]
+ * x, y: bf16 T x H.  gate_up: a stack of 2 E matrices K = H, N = I, expert
+ * e's gate at 2 e, its up at 2 e + 1; down: a stack of E matrices K = I, N = H;
+ * each bf16 or 4-bit.  ids outside [0, E) add nothing (padding, experts kept
+ * elsewhere); an expert that a token names twice counts with both weights; a
+ * token without experts gets zeros.  workspace: device memory of
+ * tg_moe_workspace_bytes(T, I, k), 16-byte aligned, not shared by calls that
+ * may overlap.  Tokens are taken 64 at a time: every 64 read the experts that
+ * they chose once.  The same call gives the same bits.
+ * Limits: H, I <= 65536 and those of tg_moe_route (TG_E_UNSUPPORTED).
+ */
+int tg_moe_workspace_bytes(int64_t T, int64_t I, int k, size_t *bytes);
+int tg_moe_mlp(int64_t T, int64_t H, int64_t I, int64_t E, int k, const void *x, const int32_t *ids,
+               const float *weights, const tg_weight *gate_up, const tg_weight *down, void *y, int gate,
+               void *workspace, size_t workspace_bytes);
+
+/*
+ * tg_moe_route and tg_moe_mlp in one call; ids and weights are outputs.
+ */
+int tg_moe_layer(int64_t T, int64_t H, int64_t I, int64_t E, int k, const void *x, const void *logits,
+                 int logits_dtype, int renorm, const tg_weight *gate_up, const tg_weight *down, void *y, int32_t *ids,
+                 float *weights, int gate, void *workspace, size_t workspace_bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,368 @@
+"""GPU parity of 4-bit weights, routing and expert layers against the fp64 oracle.
+
+Where inputs are small integers and scales powers of two, every product and
+every partial sum (of at most 2^24 units) is exact in fp32, in any order:
+fp32 results are the oracle's bits and bf16 results its rounding.  Elsewhere
+the bounds are derived beside the test: a rounding to bf16 is off by at most
+2^-8 of the value, one to fp32 by 2^-24.
+"""
+import numpy as np
+import pytest
+
+from oracle import experts_ref as R
+from tile_shape_autotuning_amd import workloads as wl
+
+from gpu_util import mark
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+tg = pytest.importorskip("tile_shape_autotuning_amd")
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _cuda(a):
+    a = np.ascontiguousarray(a)
+    return torch.from_numpy(a.view(np.int32) if a.dtype == np.uint32 else a).cuda()
+
+
+def _bf16(a):
+    return _cuda(np.asarray(a, np.float32)).to(torch.bfloat16)
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _w4(rng, lead, K, N, group, zero, scale, powers=(0.5, 1.0, 2.0)):
+    """Random 4-bit weights: the tuple for the GPU and fp64 [*lead, K, N]."""
+    P, C, G = -(-N // 16), -(-K // 128), -(-K // group)
+    n = int(np.prod(lead, dtype=int))
+    words = rng.integers(0, 2 ** 32, (n, P, C, 64, 4), dtype=np.uint32)
+    scales = rng.choice(np.array(powers, np.float32), (n, P, G, 16))
+    zeros = rng.integers(0, 16, (n, P, G, 16), dtype=np.uint8) if zero else None
+    ref = np.stack([R.dense(words[i], scales[i], None if zeros is None else zeros[i], K, N, group) for i in range(n)])
+    q = tg.W4(_cuda(words.reshape(*lead, P, C, 64, 4)),
+              _cuda(scales.reshape(*lead, P, G, 16)).to(torch.float32 if scale == "f32" else torch.bfloat16),
+              _cuda(zeros.reshape(*lead, P, G, 16)) if zero else None, K, N, group)
+    return q, ref.reshape(*lead, K, N)
+
+
+# ---------------------------------------------------------------- quantisation
+@pytest.mark.parametrize("K,N,group,zero,scale,dtype,rows", [
+    (1, 1, 32, False, "bf16", "f32", True), (128, 16, 128, False, "bf16", "bf16", True),
+    (300, 37, 32, True, "f32", "f32", True), (300, 37, 64, True, "bf16", "bf16", False),
+    (515, 65, 128, True, "f32", "f32", False), (515, 130, 256, False, "f32", "bf16", True),
+    (1000, 20, 2048, True, "bf16", "f32", False), (129, 64, 64, False, "f32", "f32", True)])
+def test_quantize_gives_the_oracles_codes(K, N, group, zero, scale, dtype, rows):
+    rng = np.random.default_rng(K + N)
+    W = rng.standard_normal((2, K, N)) * 10.0 ** rng.uniform(-3, 3, (2, 1, N)) + 0.3 * zero
+    # quotients in the middle of two codes, a group of zeros, one of a single sign, tiny numbers
+    W[0, :, 0] = rng.choice([7.0, 0.5, 1.5, -2.5, -3.5], K)
+    W[0, :, N // 2] = 0.0
+    W[1, :, 0] = np.abs(W[1, :, 0])
+    W[1, :, N - 1] *= 2.0 ** -115
+    W = R.round_bf16(W) if dtype == "bf16" else W.astype(np.float32).astype(np.float64)
+    t = _bf16(W) if dtype == "bf16" else _cuda(W.astype(np.float32))
+    if not rows:
+        t = t.transpose(1, 2).contiguous().transpose(1, 2)
+    mark(f"w4_quantize {K}x{N} g{group} zero {zero} {scale} {dtype} rows {rows}")
+    q, values = tg.w4_quantize(t, group, zero_point=zero, scale_dtype=torch.float32 if scale == "f32" else None,
+                               values=True)
+    torch.cuda.synchronize()
+    assert values.dtype == t.dtype and values.stride() == t.stride()
+    for i in range(2):
+        codes, s, z, v = R.quantize(W[i], group, zero, scale == "bf16")
+        assert np.array_equal(_np(q.scales[i]), R.panels(s))
+        if zero:
+            assert np.array_equal(q.zeros[i].cpu().numpy(), R.panels(z.astype(np.uint8)))
+        words = q.words[i].cpu().numpy().view(np.uint32)
+        assert np.array_equal(words, R.pack(codes)), "codes, and zeros past K and N"
+        # fp32 values: one product, rounded once
+        want = R.round_bf16(v) if dtype == "bf16" else v.astype(np.float32).astype(np.float64)
+        assert np.array_equal(_np(values[i]), want)
+
+
+def test_quantize_marks_groups_that_are_not_finite():
+    W = torch.ones((256, 3), device="cuda")
+    W[5, 0], W[200, 1] = float("nan"), float("inf")
+    q, v = tg.w4_quantize(W, 128, values=True)
+    bad = torch.isnan(v).cpu()
+    assert bad[:128, 0].all() and bad[128:, 1].all() and int(bad.sum()) == 256
+
+
+# ---------------------------------------------------------------- products on 4-bit weights
+GEMMS = [(1, 16, 128, 128, False, "bf16"), (1, 1, 1, 32, True, "f32"), (3, 17, 33, 32, True, "bf16"),
+         (16, 4096, 1024, 128, False, "bf16"), (17, 100, 1000, 64, True, "f32"), (33, 48, 777, 32, True, "f32"),
+         (64, 1001, 776, 256, False, "bf16"), (65, 80, 128, 32, False, "f32"), (130, 257, 640, 128, True, "bf16"),
+         (1, 40, 9000, 1024, True, "bf16"), (300, 272, 520, 64, False, "bf16"), (5, 16, 2100, 384, True, "f32"),
+         (129, 513, 1031, 128, False, "f32"), (257, 520, 2048, 32, True, "bf16"), (2, 3000, 96, 64, False, "bf16")]
+
+
+@pytest.mark.parametrize("M,N,K,group,zero,scale", GEMMS)
+def test_gemm_w4_is_exact_on_integers(M, N, K, group, zero, scale):
+    rng = np.random.default_rng(M * N + K)
+    # |A| <= 4, |q - z| <= 15, scales <= 2 in halves: sums below 4 * 47 * 2 * 9000 halves, under 2^24
+    A = rng.integers(-4, 5, (M, K)).astype(np.float64)
+    q, W = _w4(rng, (), K, N, group, zero, scale)
+    bias = rng.integers(-100, 101, N).astype(np.float32)
+    ref = A @ W
+    mark(f"gemm_w4 {M}x{N}x{K} g{group} zero {zero} {scale}")
+    C = tg.gemm_w4(_bf16(A), q, out_dtype=torch.float32)
+    B = tg.gemm_w4(_bf16(A), q, _cuda(bias), act="relu")
+    torch.cuda.synchronize()
+    assert np.array_equal(_np(C), ref)
+    assert B.dtype == torch.bfloat16 and np.array_equal(_np(B), R.round_bf16(np.maximum(ref + bias, 0.0)))
+
+
+@pytest.mark.parametrize("M,N,K,group,zero,mean", [(1, 320, 4096, 128, False, 0.0), (20, 200, 1500, 64, True, 0.0),
+                                                   (200, 300, 1032, 32, True, 1.0), (64, 64, 777, 128, False, 3.0)])
+def test_gemm_w4_on_random_rows(M, N, K, group, zero, mean):
+    rng = np.random.default_rng(7)
+    A = R.round_bf16(rng.standard_normal((M, K)) + mean)
+    q, W = _w4(rng, (), K, N, group, zero, "f32", powers=(0.3, 0.7, 1.1))
+    bias = rng.standard_normal(N).astype(np.float32)
+    v = A @ W + bias
+    ref = R.act(v, "gelu")
+    C = _np(tg.gemm_w4(_bf16(A), q, _cuda(bias), act="gelu", out_dtype=torch.float32))
+    # every term of the three sums is at most |A| (31 + 24 + 8) scale; at most 128 + 8 additions inside a
+    # group, then one a chunk, each off by 2^-23 of the terms summed (twice a rounding: the matrix cores may
+    # truncate).  GELU's slope is at most 1.13 and its own error 1.5e-7 of the value.
+    size = np.abs(A) @ np.full((K, N), 63.0 * 1.1) + np.abs(bias)
+    bound = 1.13 * (136 + K / 128 + 8) * 2.0 ** -23 * size + 4e-7 * np.abs(v)
+    assert np.all(np.abs(C - ref) <= bound)
+    # and as errors of both signs the whole stays far nearer: 2e-5 of the result is what fp32 outputs are held to
+    assert np.linalg.norm(C - ref) <= 2e-5 * np.linalg.norm(ref)
+
+
+def test_gemm_w4_keeps_what_is_around_its_output_and_repeats_itself():
+    rng = np.random.default_rng(3)
+    for M, N in ((3, 19), (70, 37), (300, 100)):
+        q, W = _w4(rng, (), 200, N, 64, True, "bf16")
+        A = torch.randn((M, 200), device="cuda", dtype=torch.bfloat16)
+        store = torch.full((M + 2, N), 77.0, device="cuda")
+        out = tg.gemm_w4(A, q, out=store[1:M + 1])
+        again = tg.gemm_w4(A, q, out_dtype=torch.float32)
+        assert torch.equal(out, again)
+        assert bool((store[0] == 77.0).all()) and bool((store[M + 1] == 77.0).all())
+
+
+def test_gemm_w4_takes_rows_off_alignment_and_spreads_nan_by_row():
+    rng = np.random.default_rng(5)
+    for M in (4, 150):
+        q, W = _w4(rng, (), 256, 48, 128, False, "bf16")
+        A = rng.integers(-4, 5, (M, 256)).astype(np.float64)
+        flat = torch.empty(M * 256 + 8, dtype=torch.bfloat16, device="cuda")
+        off = flat[1:M * 256 + 1].view(M, 256)
+        off.copy_(_bf16(A))
+        assert np.array_equal(_np(tg.gemm_w4(off, q, out_dtype=torch.float32)), A @ W)
+        off[2, 17] = float("nan")
+        C = tg.gemm_w4(off, q, out_dtype=torch.float32)
+        assert bool(torch.isnan(C[2]).all()) and int(torch.isnan(C).sum()) == 48
+    assert tg.gemm_w4(off[:0], q).shape == (0, 48)
+
+
+# ---------------------------------------------------------------- routing
+@pytest.mark.parametrize("T,E,k,renorm,dtype", [(1, 1, 1, True, "f32"), (1, 64, 6, True, "f32"),
+                                                (7, 8, 8, False, "f32"), (130, 65, 3, True, "bf16"),
+                                                (33, 256, 8, False, "bf16"), (9, 300, 16, True, "f32"),
+                                                (5, 1024, 16, False, "f32"), (1000, 128, 4, True, "bf16")])
+def test_route(T, E, k, renorm, dtype):
+    rng = np.random.default_rng(T + E)
+    v = rng.standard_normal((T, E)) * 3.0
+    v[:, E // 2:] = np.round(v[:, E // 2:])            # many ties
+    v[rng.random((T, E)) < 0.1] = -np.inf
+    v[0] = v[0, 0] if np.isfinite(v[0, 0]) else 1.0    # a row of equals
+    if T > 3:
+        v[2] = -np.inf                                 # a row whose mask leaves nothing
+        v[3, 1:] = -np.inf                             # one that it leaves one expert
+        v[3, 0] = 2.0
+    v = v.astype(np.float32)
+    if dtype == "bf16":
+        fine = np.isfinite(v)
+        v[fine] = R.round_bf16(v[fine])
+    mark(f"moe_route {T}x{E} k{k} {dtype}")
+    t = _cuda(v).to(torch.bfloat16) if dtype == "bf16" else _cuda(v)
+    ids, w = tg.moe_route(t, k, renorm=renorm)
+    torch.cuda.synchronize()
+    want, ww = R.route(v, k, renorm)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    # exp of an fp32 difference d: 2^-24 |d| from the difference, 2 units from exp, E - 1 additions, a division
+    bound = (40 * 2.0 ** -24 + 4 * 2.0 ** -24 + E * 2.0 ** -24) * ww
+    assert np.all(np.abs(_np(w) - ww) <= bound + 1e-37)
+
+
+def test_route_with_nan_and_infinity_stays_in_range():
+    v = torch.zeros((3, 20), device="cuda")
+    v[0, 7], v[1, 9] = float("nan"), float("inf")
+    v[2] = float("nan")
+    ids, w = tg.moe_route(v, 4)
+    ids = ids.cpu()
+    assert ids[0].tolist() == [7, 0, 1, 2] and ids[1].tolist() == [9, 0, 1, 2] and ids[2].tolist() == [0, 1, 2, 3]
+    assert bool(torch.isnan(w).all())
+
+
+# ---------------------------------------------------------------- expert layers
+def _experts(rng, E, H, I, kind, group=64, zero=True, scale="bf16"):
+    """Experts whose sums are exact: the GPU's weights and fp64 gate, up [E, H, I], down [E, I, H]."""
+    if kind == "w4":
+        unit = 2.0 ** -round(np.log2(max(H, 2)) / 2 + 3)
+        up, u = _w4(rng, (E, 2), H, I, group, zero, scale, powers=(unit, 2 * unit))
+        down, d = _w4(rng, (E,), I, H, group, zero, scale)
+        return up, down, u[:, 0], u[:, 1], d
+    unit = 2.0 ** -round(np.log2(max(H, 2)) / 2)
+    u = rng.integers(-2, 3, (E, 2, I, H)) * unit
+    d = rng.integers(-4, 5, (E, H, I)).astype(np.float64)
+    return _bf16(u), _bf16(d), u[:, 0].transpose(0, 2, 1), u[:, 1].transpose(0, 2, 1), d.transpose(0, 2, 1)
+
+
+def _check_mlp(y, x, ids, w, gate, up, down, act, kind):
+    ref, size = R.mlp(x, ids, w, gate, up, down, act)
+    # g and u are exact.  h: the gate's exp and division (exp2 of an fp32 product of at most 2^6: 2^-18) and its
+    # storage in two bf16 (2^-16) ; the last product: terms of up to (31 + 24 + 8) / 0.5 of a code's own size in
+    # 4 bits, (136 + chunks) additions a group, 2^-23 each; then one rounding to bf16
+    chunks = down.shape[1] / 128 * ids.shape[1] + 16
+    amp = np.max(np.abs(down)) / np.maximum(np.mean(np.abs(down)), 1e-30) * 63 if kind == "w4" else 1.0
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -15 + (136 + chunks) * 2.0 ** -23 * amp) * size * 1.01 + 1e-30
+    got = _np(y)
+    worst = np.max(np.abs(got - ref) / bound) if got.size else 0.0
+    assert worst <= 1.0, f"{worst:.3g} of the bound"
+
+
+MLPS = [(1, 4, 2, 64, 32, "bf16", "silu"), (1, 1, 1, 8, 1, "bf16", "gelu"), (3, 5, 2, 100, 37, "bf16", "silu"),
+        (16, 8, 4, 128, 200, "w4", "silu"), (17, 3, 2, 96, 130, "w4", "gelu"), (40, 2, 1, 264, 72, "bf16", "gelu"),
+        (64, 40, 6, 136, 64, "w4", "silu"), (65, 4, 3, 33, 50, "w4", "silu"), (130, 6, 2, 72, 136, "bf16", "silu"),
+        (64, 1, 1, 48, 40, "bf16", "silu"), (5, 1024, 16, 16, 16, "bf16", "silu"), (2, 3, 2, 1200, 300, "w4", "silu")]
+
+
+def _choices(rng, T, E, k):
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    w = rng.integers(1, 9, (T, k)) / 8.0
+    return ids, w.astype(np.float32)
+
+
+@pytest.mark.parametrize("T,E,k,H,I,kind,act", MLPS)
+def test_moe_mlp(T, E, k, H, I, kind, act):
+    rng = np.random.default_rng(T * E + H)
+    up, down, g, u, d = _experts(rng, E, H, I, kind)
+    x = rng.integers(-2, 3, (T, H)).astype(np.float64)
+    ids, w = _choices(rng, T, E, k)
+    mark(f"moe_mlp T{T} E{E} k{k} H{H} I{I} {kind} {act}")
+    y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down, gate=act)
+    torch.cuda.synchronize()
+    _check_mlp(y, x, ids, w.astype(np.float64), g, u, d, act, kind)
+    # ids that name nobody, one expert twice, a token without any
+    ids[rng.random((T, k)) < 0.3] = rng.choice([-1, E, 2 ** 31 - 1, -2 ** 31])
+    if k > 1:
+        ids[T // 2, 1] = ids[T // 2, 0]
+    ids[T - 1] = -1
+    again = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down, gate=act)
+    torch.cuda.synchronize()
+    _check_mlp(again, x, ids, w.astype(np.float64), g, u, d, act, kind)
+    assert not again[T - 1].any()
+
+
+@pytest.mark.parametrize("group,zero,scale", [(32, True, "f32"), (128, False, "bf16"), (256, True, "f32"),
+                                              (64, False, "bf16")])
+def test_moe_mlp_storage_forms(group, zero, scale):
+    rng = np.random.default_rng(group)
+    T, E, k, H, I = 20, 6, 3, 200, 150
+    up, down, g, u, d = _experts(rng, E, H, I, "w4", group, zero, scale)
+    x = rng.integers(-2, 3, (T, H)).astype(np.float64)
+    ids, w = _choices(rng, T, E, k)
+    y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down)
+    torch.cuda.synchronize()
+    _check_mlp(y, x, ids, w.astype(np.float64), g, u, d, "silu", "w4")
+
+
+@pytest.mark.parametrize("T,E,k,kind", [(1, 8, 2, "w4"), (4, 70, 8, "bf16"), (17, 33, 4, "w4"), (70, 9, 2, "bf16")])
+def test_moe_layer_is_route_then_mlp(T, E, k, kind):
+    rng = np.random.default_rng(T)
+    up, down, g, u, d = _experts(rng, E, 136, 80, kind)
+    x = _bf16(rng.integers(-2, 3, (T, 136)))
+    logits = torch.randn((T, E), device="cuda")
+    logits[:, :3] = 0.25
+    for t in (logits, logits.to(torch.bfloat16)):
+        for renorm in (True, False):
+            ids, w = tg.moe_route(t, k, renorm=renorm)
+            y = tg.moe_mlp(x, ids, w, up, down)
+            got, gi, gw = tg.moe_layer(x, t, up, down, k, renorm=renorm)
+            torch.cuda.synchronize()
+            assert torch.equal(gi, ids) and torch.equal(gw, w) and torch.equal(got, y)
+
+
+def test_moe_nan_stays_in_its_token_and_repeats():
+    rng = np.random.default_rng(11)
+    up, down, *_ = _experts(rng, 4, 64, 48, "w4")
+    x = torch.randn((6, 64), device="cuda", dtype=torch.bfloat16)
+    ids, w = _choices(rng, 6, 4, 2)
+    ids, w = _cuda(ids), _cuda(w)
+    clean = tg.moe_mlp(x, ids, w, up, down)
+    assert torch.equal(clean, tg.moe_mlp(x, ids, w, up, down))
+    x[2, 5] = float("nan")
+    y = tg.moe_mlp(x, ids, w, up, down)
+    assert bool(torch.isnan(y[2]).all())
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(y[keep], clean[keep])
+
+
+# ---------------------------------------------------------------- together
+def _block(x, wn, router, up, down, out, k):
+    """A decode block's feed-forward half: norm, router, experts, a 4-bit projection."""
+    h = tg.rmsnorm(x, wn, 1e-6, occupancy=1)
+    logits = tg.gemm_w4(h, router, out_dtype=torch.float32)
+    y, ids, w = tg.moe_layer(h, logits, up, down, k)
+    return tg.gemm_w4(y, out, act="relu"), ids
+
+
+def test_a_block_on_two_streams_and_in_two_graphs():
+    rng = np.random.default_rng(21)
+    H, I, E, k = 256, 96, 16, 3
+    up, down, *_ = _experts(rng, E, H, I, "w4")
+    out, _ = _w4(rng, (), H, 320, 128, False, "bf16", powers=(0.01, 0.02))
+    router, _ = _w4(rng, (), H, E, 32, True, "f32", powers=(0.01, 0.03))
+    wn = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+    xs = [torch.randn((T, H), device="cuda").to(torch.bfloat16) for T in (2, 19)]
+    want = [[t.clone() for t in _block(x, wn, router, up, down, out, k)] for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    for x, s in zip(xs, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(_block(x, wn, router, up, down, out, k))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+    graphs = []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = _block(x, wn, router, up, down, out, k)
+        graphs.append((g, r))
+    for turn in range(3):
+        for x in xs:
+            x.copy_(torch.randn(x.shape, device="cuda"))
+        want = [[t.clone() for t in _block(x, wn, router, up, down, out, k)] for x in xs]
+        for s, (g, _) in zip(streams, graphs):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, r), w in zip(graphs, want):
+            assert all(torch.equal(a, b) for a, b in zip(r, w)), f"replay {turn}"
+
+
+def test_quantised_weights_serve_the_product():
+    W = torch.randn((640, 80), device="cuda") * 0.05
+    q, v = tg.w4_quantize(W, 64, zero_point=True, scale_dtype=torch.float32, values=True)
+    eye = torch.eye(640, device="cuda", dtype=torch.bfloat16)
+    C = tg.gemm_w4(eye, q, out_dtype=torch.float32)
+    # one term a sum, but the three parts of it are added in fp32: 31 + 24 + 8 scales, 4 additions
+    step = q.scales.float().amax().item()
+    assert float((C - v).abs().max()) <= 4 * 63 * step * 2.0 ** -23

@@ -17,6 +17,7 @@ from ._native import (ACT, BF16, BF16_F32OUT, F32, Cfg, DeviceDesc, TileGemmErro
                       set_device_override, set_shape_buckets, dispatch_m, space, stats, rmsnorm_autotune,
                       set_tile_order, tile_order,
                       rmsnorm_cache_lookup, rmsnorm_tunes)
+from .experts import W4, gemm_w4, moe_layer, moe_mlp, moe_route, w4_quantize
 
 __all__ = [
     "gemm_bias_act", "gemm_autotune", "Cfg", "DeviceDesc", "TileGemmError", "F32", "BF16", "BF16_F32OUT",
@@ -26,6 +27,7 @@ __all__ = [
     "cache_clear", "cache_size", "stats", "dtype_code", "set_shape_buckets", "dispatch_m", "set_tile_order",
     "tile_order",
     "rmsnorm", "rmsnorm_autotune", "rmsnorm_cache_lookup", "rmsnorm_tunes",
+    "W4", "w4_quantize", "gemm_w4", "moe_route", "moe_mlp", "moe_layer",
 ]
 
 

@@ -13,6 +13,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libtilegemm.so")
 
 F32, BF16, BF16_F32OUT = 0, 1, 2
+W_BF16, W_W4 = 0, 1
+GATE = {"silu": 0, "gelu": 1}
 ACT = {"none": 0, "relu": 1, "gelu": 2}
 
 TG_OK, TG_E_INVAL, TG_E_INFEASIBLE, TG_E_UNSUPPORTED, TG_E_HIP, TG_E_NOMEM, TG_E_CACHE = 0, -1, -2, -3, -4, -5, -6
@@ -29,6 +31,7 @@ EXPORTS = [
     "tg_autotune_table", "tg_cache_lookup", "tg_cache_save", "tg_cache_load", "tg_cache_clear",
     "tg_cache_size", "tg_stats", "tg_set_shape_buckets", "tg_dispatch_m", "tg_set_tile_order", "tg_tile_order",
     "tg_rmsnorm", "tg_rmsnorm_autotune", "tg_rmsnorm_cache_lookup", "tg_rmsnorm_tunes",
+    "tg_w4_quantize", "tg_gemm_w4", "tg_moe_route", "tg_moe_workspace_bytes", "tg_moe_mlp", "tg_moe_layer",
 ]
 
 
@@ -72,6 +75,13 @@ class TuneRow(ctypes.Structure):
                 ("confirmed_us", ctypes.c_double)]
 
 
+class Weight(ctypes.Structure):
+    """tg_weight: a stack of matrices on the device."""
+    _fields_ = [("format", ctypes.c_int32), ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p)]
+
+
 class TileGemmError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
@@ -90,6 +100,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         i64, i32, vp, dp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.POINTER(ctypes.c_double)
         pc = ctypes.POINTER(Cfg)
+        pw = ctypes.POINTER(Weight)
         pi = ctypes.POINTER(ctypes.c_int)
         pi64 = ctypes.POINTER(ctypes.c_int64)
         sig = {
@@ -132,6 +143,13 @@ def lib():
             "tg_rmsnorm_autotune": ([i64, i64, pi, dp], i32),
             "tg_rmsnorm_cache_lookup": ([i64, i64, pi, dp, pi], i32),
             "tg_rmsnorm_tunes": ([pi64], i32),
+            "tg_w4_quantize": ([i64, i64, i64, i32, vp, i32, i32, i32, vp, vp, vp, vp], i32),
+            "tg_gemm_w4": ([i64, i64, i64, vp, pw, vp, vp, i32, i32], i32),
+            "tg_moe_route": ([i64, i64, i32, vp, i32, i32, vp, vp], i32),
+            "tg_moe_workspace_bytes": ([i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)], i32),
+            "tg_moe_mlp": ([i64, i64, i64, i64, i32, vp, vp, vp, pw, pw, vp, i32, vp, ctypes.c_size_t], i32),
+            "tg_moe_layer": ([i64, i64, i64, i64, i32, vp, vp, i32, i32, pw, pw, vp, vp, vp, i32, vp,
+                              ctypes.c_size_t], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -373,6 +391,36 @@ def rmsnorm_tunes() -> int:
     k = ctypes.c_int64()
     check(lib().tg_rmsnorm_tunes(ctypes.byref(k)))
     return k.value
+
+
+# ---------------------------------------------------------------- 4-bit weights and experts (device addresses)
+def w4_quantize_ptr(count, K, N, group, W, dtype, rows_first, scale_dtype, words, scales, zeros, values) -> int:
+    return lib().tg_w4_quantize(count, K, N, group, W, dtype, 1 if rows_first else 0, scale_dtype, words, scales,
+                                zeros, values)
+
+
+def gemm_w4_ptr(M, N, K, A, weight, bias, C, dtype, act) -> int:
+    return lib().tg_gemm_w4(M, N, K, A, weight, bias, C, dtype, act)
+
+
+def moe_route_ptr(T, E, k, logits, dtype, renorm, ids, weights) -> int:
+    return lib().tg_moe_route(T, E, k, logits, dtype, 1 if renorm else 0, ids, weights)
+
+
+def moe_workspace_bytes(T, I, k) -> int:
+    n = ctypes.c_size_t()
+    check(lib().tg_moe_workspace_bytes(T, I, k, ctypes.byref(n)))
+    return n.value
+
+
+def moe_mlp_ptr(T, H, I, E, k, x, ids, weights, gate_up, down, y, gate, workspace, workspace_bytes) -> int:
+    return lib().tg_moe_mlp(T, H, I, E, k, x, ids, weights, gate_up, down, y, gate, workspace, workspace_bytes)
+
+
+def moe_layer_ptr(T, H, I, E, k, x, logits, logits_dtype, renorm, gate_up, down, y, ids, weights, gate, workspace,
+                  workspace_bytes) -> int:
+    return lib().tg_moe_layer(T, H, I, E, k, x, logits, logits_dtype, 1 if renorm else 0, gate_up, down, y, ids,
+                              weights, gate, workspace, workspace_bytes)
 
 
 def stats():

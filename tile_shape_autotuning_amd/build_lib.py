@@ -46,6 +46,11 @@ HEADERS = [os.path.join(CSRC, f) for f in ("select.hpp", "registry.hpp", "runtim
     [os.path.join(REPO, "include", "tilegemm.h")]
 
 
+# headers of the 4-bit weight and expert kernels only
+W4_HEADERS = [os.path.join(CSRC, f) for f in ("w4.hpp", "w4_host.hpp")]
+W4_SOURCES = ("w4_quantize.hip", "gemm_w4.hip", "moe.hip")
+
+
 def kernel_source_digest() -> str:
     """SHA-256 over what decides a GEMM call's memory traffic: the GEMM
     kernel sources, the launch path (grid, block order, instantiation chosen)
@@ -288,7 +293,8 @@ def build(force: bool = True, jobs: int | None = None, verbose: bool = False) ->
 
     def compile_host(src, hip):
         obj = os.path.join(BUILD, os.path.basename(src).rsplit(".", 1)[0] + ".o")
-        if force or _stale(obj, [src] + HEADERS):
+        deps = HEADERS + (W4_HEADERS if os.path.basename(src) in W4_SOURCES else [])
+        if force or _stale(obj, [src] + deps):
             if hip:
                 _run([HIPCC, *HIP_FLAGS, "-c", src, "-o", obj], verbose)
             else:
@@ -306,6 +312,7 @@ def build(force: bool = True, jobs: int | None = None, verbose: bool = False) ->
                  ex.submit(compile_host, os.path.join(CSRC, "pad.hip"), True),
                  ex.submit(compile_host, os.path.join(CSRC, "rmsnorm.hip"), True),
                  ex.submit(compile_host, os.path.join(CSRC, "noalloc.hip"), True)]
+        hfuts += [ex.submit(compile_host, os.path.join(CSRC, f), True) for f in W4_SOURCES]
         unit_objs = [f.result() for f in futs]
         host_objs = [f.result() for f in hfuts]
 
