@@ -494,12 +494,12 @@ int tg_moe_route(int64_t T, int64_t E, int k, const void *logits, int dtype, int
  * each bf16 or 4-bit.  ids outside [0, E) add nothing (padding, experts kept
  * elsewhere); an expert that a token names twice counts with both weights; a
  * token without experts gets zeros.  workspace: device memory of
- * tg_moe_workspace_bytes(T, I, k), 16-byte aligned, not shared by calls that
+ * tg_moe_workspace_bytes(T, H, I, k), 16-byte aligned, not shared by calls that
  * may overlap.  Tokens are taken 64 at a time: every 64 read the experts that
  * they chose once.  The same call gives the same bits.
  * Limits: H, I <= 65536 and those of tg_moe_route (TG_E_UNSUPPORTED).
  */
-int tg_moe_workspace_bytes(int64_t T, int64_t I, int k, size_t *bytes);
+int tg_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int k, size_t *bytes);
 int tg_moe_mlp(int64_t T, int64_t H, int64_t I, int64_t E, int k, const void *x, const int32_t *ids,
                const float *weights, const tg_weight *gate_up, const tg_weight *down, void *y, int gate,
                void *workspace, size_t workspace_bytes);

@@ -139,7 +139,7 @@ def _mlp(layer=False, **kw):
 @pytest.mark.parametrize("kw", [dict(T=-1), dict(H=0), dict(I=0), dict(E=0), dict(k=0), dict(k=9), dict(x=None),
                                 dict(x=BUF + 1), dict(y=None), dict(ids=None), dict(weights=BUF + 2), dict(gate=2),
                                 dict(up=None), dict(down=_w4(group=40)), dict(down=_w4(data=BUF + 2, fmt=N.W_BF16)),
-                                dict(ws=None), dict(ws=BUF + 8), dict(ws_bytes=2 * 64 * 4 - 1)])
+                                dict(ws=None), dict(ws=BUF + 8), dict(ws_bytes=2 * 128 * 4 - 1)])
 def test_mlp_refuses(layer, kw):
     assert _mlp(layer, **kw) == N.TG_E_INVAL and N.last_error()
 
@@ -152,11 +152,11 @@ def test_mlp_limits_and_empty(layer):
 
 
 def test_workspace_is_for_one_pass_of_tokens():
-    assert N.moe_workspace_bytes(3, 17, 4) == 3 * 4 * 32 * 4
-    assert N.moe_workspace_bytes(1000, 17, 4) == N.moe_workspace_bytes(64, 17, 4)
+    assert N.moe_workspace_bytes(3, 10, 17, 4) == 3 * 4 * (32 + 10) * 4
+    assert N.moe_workspace_bytes(1000, 10, 17, 4) == N.moe_workspace_bytes(64, 10, 17, 4)
     n = ctypes.c_size_t()
-    assert N.lib().tg_moe_workspace_bytes(1, 0, 1, ctypes.byref(n)) == N.TG_E_INVAL
-    assert N.lib().tg_moe_workspace_bytes(1, 1, 1, None) == N.TG_E_INVAL
+    assert N.lib().tg_moe_workspace_bytes(1, 1, 0, 1, ctypes.byref(n)) == N.TG_E_INVAL
+    assert N.lib().tg_moe_workspace_bytes(1, 1, 1, 1, None) == N.TG_E_INVAL
 
 
 def test_python_refuses_cpu_tensors_and_shapes():

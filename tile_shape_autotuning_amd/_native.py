@@ -146,7 +146,7 @@ def lib():
             "tg_w4_quantize": ([i64, i64, i64, i32, vp, i32, i32, i32, vp, vp, vp, vp], i32),
             "tg_gemm_w4": ([i64, i64, i64, vp, pw, vp, vp, i32, i32], i32),
             "tg_moe_route": ([i64, i64, i32, vp, i32, i32, vp, vp], i32),
-            "tg_moe_workspace_bytes": ([i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)], i32),
+            "tg_moe_workspace_bytes": ([i64, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)], i32),
             "tg_moe_mlp": ([i64, i64, i64, i64, i32, vp, vp, vp, pw, pw, vp, i32, vp, ctypes.c_size_t], i32),
             "tg_moe_layer": ([i64, i64, i64, i64, i32, vp, vp, i32, i32, pw, pw, vp, vp, vp, i32, vp,
                               ctypes.c_size_t], i32),
@@ -407,9 +407,9 @@ def moe_route_ptr(T, E, k, logits, dtype, renorm, ids, weights) -> int:
     return lib().tg_moe_route(T, E, k, logits, dtype, 1 if renorm else 0, ids, weights)
 
 
-def moe_workspace_bytes(T, I, k) -> int:
+def moe_workspace_bytes(T, H, I, k) -> int:
     n = ctypes.c_size_t()
-    check(lib().tg_moe_workspace_bytes(T, I, k, ctypes.byref(n)))
+    check(lib().tg_moe_workspace_bytes(T, H, I, k, ctypes.byref(n)))
     return n.value
 
 

@@ -1,19 +1,13 @@
 // C = act(A . W + bias), W in 4 bits with group scales (storage and
 // arithmetic: w4.hpp).
 //
-// The streaming kernel.  With few rows every weight is used once and the
-// kernel is bound by the stream of words from HBM.  A workgroup owns NT panels
-// of 16 columns and MT tiles of 16 rows; its W waves take interleaved chunks of
-// 128 rows of W (adjacent waves read adjacent KiB), one 16-byte load a lane and
-// panel.  A's fragments come straight from L2: no two waves of a workgroup
-// need the same ones.  The next chunk's loads are issued before the current
-// chunk's MFMAs.  Sums over a group stay in their own accumulators until the
-// group's scale multiplies them into the fp32 totals; the waves' totals meet
-// in LDS in wave order, so results do not depend on timing.
+// Few rows: the panels of W stream past rows kept in registers (panel_stream.hpp).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <string>
 
+#include "panel_stream.hpp"
 #include "w4.hpp"
 #include "w4_host.hpp"
 
@@ -26,105 +20,103 @@ struct GemmW4Params {
     void* C;
     int64_t M, N, K;
     int panels, out_bf16, act;
+    int per, blocks;                                   // panels a workgroup, blocks of K
 };
 
-// GS: MFMA steps (of 32 rows) between two scales: 1, 2 or 4 (a whole chunk)
-template <int MT, int NT, int W, int GS, bool VEC>
-__global__ void __launch_bounds__(64 * W) gemm_w4_stream_kernel(GemmW4Params p)
+// Bias, activation and conversion of a 16 x 16 tile whose lane holds rows
+// 4 (lane / 16) + 0..3 of column lane % 16.
+__device__ __forceinline__ void store_tile(const GemmW4Params& p, int64_t row, int64_t col, f32x4_t v, int lane)
 {
-    __shared__ f32x4_t red[W * MT * NT * 64];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, kq = lane >> 4;
-    const int panel0 = blockIdx.x * NT;
-    const int64_t row0 = (int64_t)blockIdx.y * (16 * MT);
-    const bool zero = p.w.zeros != nullptr;
-
-    struct Buf {
-        PanelChunk<true, NT, GS> w;
-        u32x4_t a[MT][1][4];
-    };
-    auto load = [&](int c, Buf& b) {
+    col += lane & 15;
+    row += (lane >> 4) * 4;
+    if (col >= p.N)
+        return;
+    const float bias = p.bias ? p.bias[col] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-            b.w.load_w4(p.w, j, min(panel0 + j, p.panels - 1), c, lane);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int64_t row = row0 + 16 * m + l16;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                b.a[m][0][t] = row < p.M ? load8<VEC>(p.A + row * p.K, (int64_t)c * 128 + 32 * t + 8 * kq, p.K)
-                                         : splat4(0);
-        }
-    };
-
-    const f32x4_t none = {0.f, 0.f, 0.f, 0.f};
-    f32x4_t total[MT][NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            total[m][j] = none;
-
-    auto use = [&](const Buf& b) { mac_chunk<true, MT, NT, 1, GS>(total, b.a, b.w, zero, ~0u); };
-
-    Buf buf[2];
-    int c = wave;
-    if (c < p.w.chunks)
-        load(c, buf[0]);
-    for (; c < p.w.chunks; c += 2 * W) {
-        if (c + W < p.w.chunks)
-            load(c + W, buf[1]);
-        use(buf[0]);
-        if (c + W < p.w.chunks) {
-            if (c + 2 * W < p.w.chunks)
-                load(c + 2 * W, buf[0]);
-            use(buf[1]);
-        }
-    }
-
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            red[((m * NT + j) * W + wave) * 64 + lane] = total[m][j];
-    __syncthreads();
-    // tile i of the workgroup's MT x NT is finished by wave i % W
-    for (int i = wave; i < MT * NT; i += W) {
-        f32x4_t v = none;
-#pragma unroll
-        for (int q = 0; q < W; ++q)
-            v += red[(i * W + q) * 64 + lane];
-        const int64_t col = (int64_t)(panel0 + i % NT) * 16 + l16;
-        if (col >= p.N)
-            continue;
-        const float bias = p.bias ? p.bias[col] : 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t row = row0 + (i / NT) * 16 + kq * 4 + r;
-            if (row >= p.M)
-                continue;
-            const float x = apply_act(v[r] + bias, p.act);
-            if (p.out_bf16)
-                static_cast<unsigned short*>(p.C)[row * p.N + col] = f32_to_bf16_rne(x);
-            else
-                static_cast<float*>(p.C)[row * p.N + col] = x;
-        }
+    for (int r = 0; r < 4; ++r) {
+        if (row + r >= p.M)
+            return;
+        const float x = apply_act(v[r] + bias, p.act);
+        if (p.out_bf16)
+            static_cast<unsigned short*>(p.C)[(row + r) * p.N + col] = f32_to_bf16_rne(x);
+        else
+            static_cast<float*>(p.C)[(row + r) * p.N + col] = x;
     }
 }
 
-template <int MT, int NT, int W>
-static int launch_stream(const GemmW4Params& p, bool vec, hipStream_t s)
+// One workgroup a compute unit: most of its LDS may hold sums.
+template <int MT>
+constexpr int kHalf = MT == 4 ? 32 : 64;
+
+// A workgroup multiplies MT x 16 rows with p.per panels (panel_stream.hpp).  K
+// beyond the waves' W x CW chunks comes in further blocks, whose sums wait in
+// LDS.
+template <bool ZERO, int MT, int W, int CW, int GS>
+__global__ void __launch_bounds__(64 * W) gemm_w4_panels_kernel(GemmW4Params p)
 {
-    const dim3 grid((unsigned)ceil_div(p.panels, NT), (unsigned)ceil_div(p.M, 16 * MT)), block(64 * W);
-    const int gs = p.w.group >= 128 ? 4 : p.w.group / 32;
-#define TG_LAUNCH(GS, VEC) hipLaunchKernelGGL((gemm_w4_stream_kernel<MT, NT, W, GS, VEC>), grid, block, 0, s, p)
-    if (vec) {
-        if (gs == 4) TG_LAUNCH(4, true); else if (gs == 2) TG_LAUNCH(2, true); else TG_LAUNCH(1, true);
+    using S = PanelStream<true, ZERO, MT, 1, 1, W, CW, GS, kHalf<MT>>;
+    __shared__ f32x4_t red[S::RED], mid[S::MID];
+    extern __shared__ f32x4_t part[];                  // [p.per][MT][64] if there is more than one block
+    S s(red, mid, p.w.scale_f32);
+    const int lane = s.lane, l16 = lane & 15, kq = lane >> 4;
+    const int panel0 = blockIdx.x * p.per;
+    const int n = min(p.per, p.panels - panel0);
+    const int64_t row0 = (int64_t)blockIdx.y * (16 * MT);
+    const int K = (int)p.K;
+
+    auto rows = [&](int block) {
+        const int c0 = (block * W + s.wave) * CW;
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    s.a[i][m][0][t] = splat4(0);
+                const int64_t row = row0 + 16 * m + l16;
+                if (c0 + i < p.w.chunks && row < p.M)
+                    load_chunk(s.a[i][m][0], p.A + row * p.K, c0 + i, kq, K);
+            }
+    };
+    auto load = [&](int block, int index, typename S::Words& b, bool some) {
+        s.load_w4(b, 0, p.w, panel0 + index, (block * W + s.wave) * CW, some);
+    };
+    auto done = [&](int block, int index, int m, f32x4_t (&sum)[1]) {
+        f32x4_t* held = part + (index * MT + m) * 64 + lane;
+        if (block > 0)
+            sum[0] += *held;
+        if (block + 1 < p.blocks)
+            *held = sum[0];
+        else
+            store_tile(p, row0 + 16 * m, (int64_t)(panel0 + index) * 16, sum[0], fresh(lane));
+    };
+    s.run(p.blocks, n, rows, load, done);
+}
+
+template <int MT, int W, int CW>
+static int launch_panels(GemmW4Params p, int per, hipStream_t s)
+{
+    p.blocks = (int)ceil_div(p.w.chunks, W * CW);
+    // the sums of K's earlier blocks wait in what LDS is left
+    using S = PanelStream<true, true, MT, 1, 1, W, CW, 1, kHalf<MT>>;
+    constexpr size_t used = (S::RED + S::MID) * sizeof(f32x4_t);
+    static_assert(used + MT * 1024 <= kLdsBytes, "LDS");
+    if (p.blocks > 1)
+        per = (int)std::min<size_t>(per, (kLdsBytes - used) / (MT * 1024));
+    p.per = per;
+    const size_t lds = p.blocks > 1 ? (size_t)per * MT * 1024 : 0;
+    const dim3 grid((unsigned)ceil_div(p.panels, per), (unsigned)ceil_div(p.M, 16 * MT)), block(64 * W);
+    if (p.w.zeros) {
+        if (p.w.group >= 128)
+            hipLaunchKernelGGL((gemm_w4_panels_kernel<true, MT, W, CW, 4>), grid, block, lds, s, p);
+        else
+            hipLaunchKernelGGL((gemm_w4_panels_kernel<true, MT, W, CW, 1>), grid, block, lds, s, p);
     } else {
-        if (gs == 4) TG_LAUNCH(4, false); else if (gs == 2) TG_LAUNCH(2, false); else TG_LAUNCH(1, false);
+        if (p.w.group >= 128)
+            hipLaunchKernelGGL((gemm_w4_panels_kernel<false, MT, W, CW, 4>), grid, block, lds, s, p);
+        else
+            hipLaunchKernelGGL((gemm_w4_panels_kernel<false, MT, W, CW, 1>), grid, block, lds, s, p);
     }
-#undef TG_LAUNCH
     return launched("gemm_w4 launch");
 }
 
@@ -165,11 +157,16 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
     p.panels = (int)ceil_div(N, 16);
     p.out_bf16 = dtype == TG_BF16;
     p.act = act;
-    const bool vec = K % 8 == 0 && ((uintptr_t)A & 15u) == 0;
     hipStream_t s = current_stream();
+    // A workgroup a compute unit, with equal shares of the panels.  Measured on
+    // 16 x 28672 x 8192: 7 panels for each of 256 workgroups 26.7 us, 8 for 224
+    // 28.5, 4 for 448 40 (two thirds of which start when others end); 16 waves
+    // of 2 chunks 26.7, 8 of 4 28.6, 8 of 2 31.6.  With more rows A's fragments
+    // leave room for fewer waves.
+    const int per = (int)ceil_div(p.panels, kCus);
     if (M <= 16)
-        return launch_stream<1, 1, 8>(p, vec, s);
+        return p.w.chunks <= 16 ? launch_panels<1, 16, 1>(p, per, s) : launch_panels<1, 16, 2>(p, per, s);
     if (M <= 32)
-        return launch_stream<2, 2, 8>(p, vec, s);
-    return launch_stream<4, 2, 8>(p, vec, s);
+        return launch_panels<2, 16, 1>(p, per, s);
+    return launch_panels<4, 8, 2>(p, per, s);
 }

@@ -23,7 +23,9 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
+#include "panel_stream.hpp"
 #include "w4.hpp"
 #include "w4_host.hpp"
 
@@ -184,10 +186,12 @@ struct MoeParams {
     const int32_t* ids;                                // [T][k]
     const float* weights;
     unsigned* h;                                       // [T k][stride], two bf16: high half + low half
+    float* yp;                                         // [T k][H], each pair's part of y
     unsigned short* y;                                 // [T][H]
     ExpertStack up, down;
     int64_t stride;                                    // I rounded up to 16
     int T, E, k, H, I, gelu;
+    int up_per, up_blocks, down_per, down_blocks;      // panels a workgroup, blocks of the reduction
 };
 
 // The tokens that chose expert e, one a lane: lane r holds the r-th one's pair
@@ -263,300 +267,297 @@ __device__ __forceinline__ float gated(float g, float u, int gelu)
     return (gelu ? gelu_erf(g) : g / (1.0f + __expf(-g))) * u;
 }
 
-template <bool W4F, int MT, int W, int GS, bool VEC>
-__global__ void __launch_bounds__(64 * W) moe_up_kernel(MoeParams p)
-{
-    __shared__ f32x4_t red[2 * W * MT * 64];
-    __shared__ int ids[kTokens * kMaxChoices];
-    __shared__ unsigned bits[kExpertWords];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, kq = lane >> 4;
-    const int panel = blockIdx.x;
+// The wave's share of a workgroup's work on one chosen expert: a stream of the
+// expert's panels past MT x 16 of its rows (panel_stream.hpp).
+struct Share {
+    int expert, rows, pair;                            // lane r: the r-th row's pair
+    float weight;
+};
 
+// False if there is no `slot`-th chosen expert.
+__device__ __forceinline__ bool share_of(const MoeParams& p, int slot, int* ids, unsigned* bits, const float* weights,
+                                         int lane, Share& s)
+{
     mark_experts(p.ids, p.T * p.k, p.E, ids, bits);
     const Chosen chosen(bits, lane);
-    if ((int)blockIdx.y >= chosen.count)
-        return;
-    const int e = chosen.expert(blockIdx.y);
-    int pair;
-    float weight;
-    const int rows = rows_of(ids, p.weights, p.T, p.k, e, lane, pair, weight);
+    if (slot >= chosen.count)
+        return false;
+    s.expert = chosen.expert(slot);
+    s.rows = rows_of(ids, weights, p.T, p.k, s.expert, lane, s.pair, s.weight);
+    return true;
+}
 
+template <bool W4F, bool ZERO, int MT, int W, int CW, int GS, bool VEC>
+__global__ void __launch_bounds__(64 * W) moe_up_kernel(MoeParams p)
+{
+    using S = PanelStream<W4F, ZERO, MT, 2, 1, W, CW, GS, 32>;
+    __shared__ f32x4_t red[S::RED], mid[S::MID];
+    __shared__ int ids[kTokens * kMaxChoices];
+    __shared__ unsigned bits[kExpertWords];
+    extern __shared__ f32x4_t part[];                  // [p.per][MT][2][64] if there is more than one block
+    S s(red, mid, p.up.w4.scale_f32);
+    const int lane = s.lane, l16 = lane & 15, kq = lane >> 4;
+    Share e;
+    if (!share_of(p, blockIdx.y, ids, bits, p.weights, lane, e))
+        return;
+    const int panel0 = blockIdx.x * p.up_per;
+    const int n = min(p.up_per, p.up.panels - panel0);
+    const int chunks = (p.H + 127) / 128;
     W4View v[2];
     const unsigned short* wb[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if constexpr (W4F)
-            v[j] = matrix(p.up, 2 * (int64_t)e + j);
+            v[j] = matrix(p.up, 2 * (int64_t)e.expert + j);
         else
-            wb[j] = p.up.bf16 + (2 * (int64_t)e + j) * p.I * p.H;
+            wb[j] = p.up.bf16 + (2 * (int64_t)e.expert + j) * p.I * p.H;
     }
-    const int64_t col = min((int64_t)panel * 16 + l16, (int64_t)p.I - 1);
-    const int chunks = (p.H + 127) / 128;
-    const bool zero = W4F && p.up.w4.zeros;
 
-    for (int r0 = 0; r0 < rows; r0 += 16 * MT) {
-        const unsigned short* xr[MT];
-        bool in[MT];
-        unsigned tiles = 0;
+    for (int r0 = 0; r0 < e.rows; r0 += 16 * MT) {
+        auto rows = [&](int block) {
+            const int c0 = (block * W + s.wave) * CW;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int r = r0 + 16 * m + l16;
-            in[m] = r < rows;
-            xr[m] = p.x + (int64_t)(__shfl(pair, r & 63) / p.k) * p.H;
-            tiles |= r0 + 16 * m < rows ? 1u << m : 0u;
-        }
-        struct Buf {
-            PanelChunk<W4F, 2, GS> w;
-            u32x4_t a[MT][1][4];
+            for (int m = 0; m < MT; ++m) {
+                const int r = r0 + 16 * m + l16;
+                const unsigned short* x = p.x + (int64_t)(__shfl(e.pair, r & 63) / p.k) * p.H;
+#pragma unroll
+                for (int i = 0; i < CW; ++i) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        s.a[i][m][0][t] = splat4(0);
+                    if (r < e.rows && c0 + i < chunks)
+                        load_chunk(s.a[i][m][0], x, c0 + i, kq, p.H);
+                }
+            }
         };
-        auto load = [&](int c, Buf& b) {
+        auto load = [&](int block, int index, typename S::Words& b, bool some) {
+            const int c0 = (block * W + s.wave) * CW;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if constexpr (W4F)
-                    b.w.load_w4(v[j], j, panel, c, lane);
+                    s.load_w4(b, j, v[j], panel0 + index, c0, some);
                 else
-                    b.w.template load_bf16<VEC>(wb[j], j, col, c, p.H, lane);
+                    s.template load_bf16<VEC>(b, j, wb[j], p.I, p.H, panel0 + index, c0, some);
             }
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    b.a[m][0][t] = in[m] ? load8<VEC>(xr[m], (int64_t)c * 128 + 32 * t + 8 * kq, p.H) : splat4(0);
         };
-        f32x4_t total[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            total[m][0] = total[m][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        Buf buf[2];
-        int c = wave;
-        if (c < chunks)
-            load(c, buf[0]);
-        for (; c < chunks; c += 2 * W) {
-            if (c + W < chunks)
-                load(c + W, buf[1]);
-            mac_chunk<W4F, MT, 2, 1, GS>(total, buf[0].a, buf[0].w, zero, tiles);
-            if (c + W < chunks) {
-                if (c + 2 * W < chunks)
-                    load(c + 2 * W, buf[0]);
-                mac_chunk<W4F, MT, 2, 1, GS>(total, buf[1].a, buf[1].w, zero, tiles);
+        auto done = [&](int block, int index, int m, f32x4_t (&sum)[2]) {
+            f32x4_t* held = part + (index * MT + m) * 128 + lane;
+            if (block > 0) {
+                sum[0] += held[0];
+                sum[1] += held[64];
             }
-        }
-        __syncthreads();                               // the previous rows' sums have been read
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                red[((m * 2 + j) * W + wave) * 64 + lane] = total[m][j];
-        __syncthreads();
-        for (int m = wave; m < MT; m += W) {
-            f32x4_t g = {0.f, 0.f, 0.f, 0.f}, u = g;
-#pragma unroll
-            for (int q = 0; q < W; ++q) {
-                g += red[((m * 2) * W + q) * 64 + lane];
-                u += red[((m * 2 + 1) * W + q) * 64 + lane];
+            if (block + 1 < p.up_blocks) {
+                held[0] = sum[0];
+                held[64] = sum[1];
+                return;
             }
+            const int at = fresh(lane), col = (panel0 + index) * 16 + (at & 15);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = r0 + 16 * m + kq * 4 + r;
-                const int to = __shfl(pair, row & 63);
-                const float w = __shfl(weight, row & 63);
-                if (row >= rows)
+                const int row = r0 + 16 * m + (at >> 4) * 4 + r;
+                const int to = __shfl(e.pair, row & 63);
+                const float w = __shfl(e.weight, row & 63);
+                if (row >= e.rows)
                     continue;
-                float hv = 0.0f;                       // columns past I stay zero for the second kernel
-                if (panel * 16 + l16 < p.I)
-                    hv = w * gated(g[r], u[r], p.gelu);
+                // columns past I stay zero for the second kernel
+                const float hv = col < p.I ? w * gated(sum[0][r], sum[1][r], p.gelu) : 0.0f;
                 const unsigned short hi = f32_to_bf16_rne(hv);
                 const float rest = hv - __uint_as_float((unsigned)hi << 16);
                 // an infinity or NaN stays one: its rest is no number
                 const unsigned short lo = (hi & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : (unsigned short)0;
-                p.h[(int64_t)to * p.stride + panel * 16 + l16] = (unsigned)hi << 16 | lo;
+                p.h[(int64_t)to * p.stride + col] = (unsigned)hi << 16 | lo;
             }
-        }
+        };
+        s.run(p.up_blocks, n, rows, load, done);
     }
 }
 
-// NTOK: tokens that the waves' tiles hold (16 or 64)
-template <bool W4F, int MT, int NTOK, int W, int GS, bool VEC>
+template <bool W4F, bool ZERO, int MT, int W, int CW, int GS, bool VEC>
 __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p)
 {
-    __shared__ float tile[W][NTOK][16];
-    __shared__ int ids[NTOK * kMaxChoices];
+    using S = PanelStream<W4F, ZERO, MT, 1, 2, W, CW, GS, 32>;
+    __shared__ f32x4_t red[S::RED], mid[S::MID];
+    __shared__ int ids[kTokens * kMaxChoices];
     __shared__ unsigned bits[kExpertWords];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, kq = lane >> 4;
-    const int panel = blockIdx.x;
+    extern __shared__ f32x4_t part[];                  // [p.per][MT][64] if there is more than one block
+    S s(red, mid, p.down.w4.scale_f32);
+    const int lane = s.lane, l16 = lane & 15, kq = lane >> 4;
+    Share e;
+    if (!share_of(p, blockIdx.y, ids, bits, nullptr, lane, e))
+        return;
+    const int panel0 = blockIdx.x * p.down_per;
+    const int n = min(p.down_per, p.down.panels - panel0);
+    W4View v;
+    const unsigned short* wb = nullptr;
+    if constexpr (W4F)
+        v = matrix(p.down, e.expert);
+    else
+        wb = p.down.bf16 + (int64_t)e.expert * p.H * p.I;
 
-#pragma unroll
-    for (int i = 0; i < NTOK / 4; ++i)
-        tile[wave][i * 4 + kq][l16] = 0.0f;
-    mark_experts(p.ids, p.T * p.k, p.E, ids, bits);
-    const Chosen chosen(bits, lane);
-    const int64_t col = min((int64_t)panel * 16 + l16, (int64_t)p.H - 1);
-    const int chunks = (p.I + 127) / 128;
-    const bool zero = W4F && p.down.w4.zeros;
-    const int64_t units = (int64_t)chosen.count * chunks;
-    int64_t at = wave * units / W;
-    const int64_t end = (wave + 1) * units / W;
-
-    while (at < end) {
-        const int slot = (int)(at / chunks);
-        const int c0 = (int)(at - (int64_t)slot * chunks);
-        const int c1 = (int)min((int64_t)chunks, c0 + (end - at));
-        at += c1 - c0;
-        const int e = chosen.expert(slot);
-        int pair;
-        float unused;
-        const int rows = rows_of(ids, nullptr, p.T, p.k, e, lane, pair, unused);
-        W4View v;
-        const unsigned short* wb = nullptr;
-        if constexpr (W4F)
-            v = matrix(p.down, e);
-        else
-            wb = p.down.bf16 + (int64_t)e * p.H * p.I;
-
-        for (int r0 = 0; r0 < rows; r0 += 16 * MT) {
-            const unsigned* hr[MT];
-            bool in[MT];
-            unsigned tiles = 0;
+    for (int r0 = 0; r0 < e.rows; r0 += 16 * MT) {
+        auto rows = [&](int block) {
+            const int c0 = (block * W + s.wave) * CW;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int r = r0 + 16 * m + l16;
-                in[m] = r < rows;
-                hr[m] = p.h + (int64_t)__shfl(pair, r & 63) * p.stride;
-                tiles |= r0 + 16 * m < rows ? 1u << m : 0u;
-            }
-            struct Buf {
-                PanelChunk<W4F, 1, GS> w;
-                u32x4_t h[MT][4][2];
-            };
-            auto load = [&](int c, Buf& b) {
-                if constexpr (W4F)
-                    b.w.load_w4(v, 0, panel, c, lane);
-                else
-                    b.w.template load_bf16<VEC>(wb, 0, col, c, p.I, lane);
+                const unsigned* h = p.h + (int64_t)__shfl(e.pair, r & 63) * p.stride;
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int i = 0; i < CW; ++i)
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const int64_t k = (int64_t)c * 128 + 32 * t + 8 * kq;
-                        b.h[m][t][0] = b.h[m][t][1] = splat4(0);
-                        if (in[m] && k < p.stride) {
-                            b.h[m][t][0] = *reinterpret_cast<const u32x4_t*>(hr[m] + k);
-                            b.h[m][t][1] = *reinterpret_cast<const u32x4_t*>(hr[m] + k + 4);
+                        const int64_t k = (int64_t)(c0 + i) * 128 + 32 * t + 8 * kq;
+                        u32x4_t h0 = splat4(0), h1 = splat4(0);
+                        if (r < e.rows && k < p.stride) {
+                            h0 = *reinterpret_cast<const u32x4_t*>(h + k);
+                            h1 = *reinterpret_cast<const u32x4_t*>(h + k + 4);
                         }
-                    }
-            };
-            f32x4_t total[MT][1];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                total[m][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            auto use = [&](const Buf& b) {
-                u32x4_t a[MT][2][4];
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
 #pragma unroll
                         for (int d = 0; d < 4; ++d) {
-                            const unsigned x0 = b.h[m][t][d >> 1][2 * (d & 1)], x1 = b.h[m][t][d >> 1][2 * (d & 1) + 1];
-                            a[m][0][t][d] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
-                            a[m][1][t][d] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
+                            const unsigned x0 = d < 2 ? h0[2 * d] : h1[2 * d - 4];
+                            const unsigned x1 = d < 2 ? h0[2 * d + 1] : h1[2 * d - 3];
+                            s.a[i][m][0][t][d] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+                            s.a[i][m][1][t][d] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
                         }
-                mac_chunk<W4F, MT, 1, 2, GS>(total, a, b.w, zero, tiles);
-            };
-            Buf buf[2];
-            load(c0, buf[0]);
-            for (int c = c0; c < c1; c += 2) {
-                if (c + 1 < c1)
-                    load(c + 1, buf[1]);
-                use(buf[0]);
-                if (c + 1 < c1) {
-                    if (c + 2 < c1)
-                        load(c + 2, buf[0]);
-                    use(buf[1]);
-                }
+                    }
             }
+        };
+        auto load = [&](int block, int index, typename S::Words& b, bool some) {
+            const int c0 = (block * W + s.wave) * CW;
+            if constexpr (W4F)
+                s.load_w4(b, 0, v, panel0 + index, c0, some);
+            else
+                s.template load_bf16<VEC>(b, 0, wb, p.H, p.I, panel0 + index, c0, some);
+        };
+        auto done = [&](int block, int index, int m, f32x4_t (&sum)[1]) {
+            f32x4_t* held = part + (index * MT + m) * 64 + lane;
+            if (block > 0)
+                sum[0] += *held;
+            if (block + 1 < p.down_blocks) {
+                *held = sum[0];
+                return;
+            }
+            const int at = fresh(lane), col = (panel0 + index) * 16 + (at & 15);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = r0 + 16 * m + kq * 4 + r;
-                    const int t = __shfl(pair, row & 63) / p.k;
-                    if (row < rows)
-                        tile[wave][t][l16] += total[m][0][r];
-                }
-        }
+            for (int r = 0; r < 4; ++r) {
+                const int row = r0 + 16 * m + (at >> 4) * 4 + r;
+                const int from = __shfl(e.pair, row & 63);
+                if (row < e.rows && col < p.H)
+                    p.yp[(int64_t)from * p.H + col] = sum[0][r];
+            }
+        };
+        s.run(p.down_blocks, n, rows, load, done);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.T * 16; i += 64 * W) {
-        const int t = i >> 4;
-        float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < W; ++q)
-            v += tile[q][t][i & 15];
-        if (panel * 16 + (i & 15) < p.H)
-            p.y[(int64_t)t * p.H + panel * 16 + (i & 15)] = f32_to_bf16_rne(v);
+}
+
+// y[t] = sum of the token's pairs, in the order of its choices.  Pairs that the
+// other kernels left out (no such expert, an expert's second mention) are
+// skipped here by the same rule.
+__global__ void __launch_bounds__(256) moe_sum_kernel(MoeParams p)
+{
+    const int t = blockIdx.y, col = blockIdx.x * 256 + threadIdx.x;
+    const int32_t* ids = p.ids + t * p.k;
+    if (col >= p.H)
+        return;
+    float v = 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+        bool first = ids[j] >= 0 && ids[j] < p.E;
+        for (int i = 0; i < j; ++i)
+            first = first && ids[i] != ids[j];
+        if (first)
+            v += p.yp[((int64_t)t * p.k + j) * p.H + col];
+    }
+    p.y[(int64_t)t * p.H + col] = f32_to_bf16_rne(v);
+}
+
+// Panels of a workgroup: two workgroups a compute unit over all chosen experts
+// (at most), as far as the sums of the reduction's earlier blocks find room in
+// LDS beside the `used` bytes.
+static int panels_per(int panels, int slots, int blocks, size_t used, size_t panel_bytes)
+{
+    int64_t per = std::max<int64_t>(1, (int64_t)panels * slots / (2 * kCus));
+    if (blocks > 1)
+        per = std::min<int64_t>(per, (int64_t)((kLdsBytes - used) / panel_bytes));
+    return (int)std::min<int64_t>(per, panels);
+}
+
+template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
+static void run_up(MoeParams p, hipStream_t s)
+{
+    constexpr int W = 8;
+    using S = PanelStream<W4F, ZERO, MT, 2, 1, W, CW, GS, 32>;
+    constexpr size_t used = (S::RED + S::MID) * 16 + (kTokens * kMaxChoices + kExpertWords) * 4;
+    static_assert(used + MT * 2048 <= kLdsBytes, "LDS");
+    const int slots = std::min(p.E, p.T * p.k);
+    p.up_blocks = (int)ceil_div(ceil_div(p.H, 128), W * CW);
+    p.up_per = panels_per(p.up.panels, slots, p.up_blocks, used, MT * 2048);
+    const size_t lds = p.up_blocks > 1 ? (size_t)p.up_per * MT * 2048 : 0;
+    const dim3 grid((unsigned)ceil_div(p.up.panels, p.up_per), (unsigned)slots);
+    hipLaunchKernelGGL((moe_up_kernel<W4F, ZERO, MT, W, CW, GS, VEC>), grid, dim3(64 * W), lds, s, p);
+}
+
+template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
+static void run_down(MoeParams p, hipStream_t s)
+{
+    constexpr int W = 8;
+    using S = PanelStream<W4F, ZERO, MT, 1, 2, W, CW, GS, 32>;
+    constexpr size_t used = (S::RED + S::MID) * 16 + (kTokens * kMaxChoices + kExpertWords) * 4;
+    static_assert(used + MT * 1024 <= kLdsBytes, "LDS");
+    const int slots = std::min(p.E, p.T * p.k);
+    p.down_blocks = (int)ceil_div(ceil_div(p.I, 128), W * CW);
+    p.down_per = panels_per(p.down.panels, slots, p.down_blocks, used, MT * 1024);
+    const size_t lds = p.down_blocks > 1 ? (size_t)p.down_per * MT * 1024 : 0;
+    const dim3 grid((unsigned)ceil_div(p.down.panels, p.down_per), (unsigned)slots);
+    hipLaunchKernelGGL((moe_down_kernel<W4F, ZERO, MT, W, CW, GS, VEC>), grid, dim3(64 * W), lds, s, p);
+}
+
+// Picks the instantiation for a weight: f.template go<W4F, ZERO, MT, CW, GS, VEC>(p, s).
+template <class F>
+static void dispatch(const tg_weight& w, int T, int64_t K, const MoeParams& p, hipStream_t s)
+{
+    const bool many = T > 16;
+    if (w.format == TG_W_W4) {
+        const bool two = K > 1024;                     // chunks a wave
+        auto pick = [&](auto zero, auto gs) {
+            constexpr bool Z = decltype(zero)::value;
+            constexpr int G = decltype(gs)::value;
+            if (many)
+                two ? F::template go<true, Z, 2, 2, G, true>(p, s) : F::template go<true, Z, 2, 1, G, true>(p, s);
+            else
+                two ? F::template go<true, Z, 1, 2, G, true>(p, s) : F::template go<true, Z, 1, 1, G, true>(p, s);
+        };
+        using One = std::integral_constant<int, 1>;
+        using Four = std::integral_constant<int, 4>;
+        if (w.zeros)
+            w.group >= 128 ? pick(std::true_type{}, Four{}) : pick(std::true_type{}, One{});
+        else
+            w.group >= 128 ? pick(std::false_type{}, Four{}) : pick(std::false_type{}, One{});
+    } else if (K % 8 == 0) {
+        many ? F::template go<false, false, 2, 1, 4, true>(p, s) : F::template go<false, false, 1, 1, 4, true>(p, s);
+    } else {
+        many ? F::template go<false, false, 2, 1, 4, false>(p, s) : F::template go<false, false, 1, 1, 4, false>(p, s);
     }
 }
 
-template <bool W4F, int MT, int GS, bool VEC>
-static void run_up(const MoeParams& p, dim3 grid, hipStream_t s)
-{
-    hipLaunchKernelGGL((moe_up_kernel<W4F, MT, 8, GS, VEC>), grid, dim3(512), 0, s, p);
-}
-
-template <bool W4F, int GS, bool VEC>
-static void run_up_rows(const MoeParams& p, dim3 grid, hipStream_t s)
-{
-    if (p.T <= 16)
-        run_up<W4F, 1, GS, VEC>(p, grid, s);
-    else if (p.T <= 32)
-        run_up<W4F, 2, GS, VEC>(p, grid, s);
-    else
-        run_up<W4F, 4, GS, VEC>(p, grid, s);
-}
-
-template <bool W4F, int GS, bool VEC>
-static void run_down_rows(const MoeParams& p, dim3 grid, hipStream_t s)
-{
-    if (p.T <= 16)
-        hipLaunchKernelGGL((moe_down_kernel<W4F, 1, 16, 8, GS, VEC>), grid, dim3(512), 0, s, p);
-    else
-        hipLaunchKernelGGL((moe_down_kernel<W4F, 2, 64, 8, GS, VEC>), grid, dim3(512), 0, s, p);
-}
-
-static int steps_per_scale(int group) { return group >= 128 ? 4 : group / 32; }
+struct Up {
+    template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
+    static void go(const MoeParams& p, hipStream_t s) { run_up<W4F, ZERO, MT, CW, GS, VEC>(p, s); }
+};
+struct Down {
+    template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
+    static void go(const MoeParams& p, hipStream_t s) { run_down<W4F, ZERO, MT, CW, GS, VEC>(p, s); }
+};
 
 static int launch_pass(const MoeParams& p, const tg_weight& up, const tg_weight& down, hipStream_t s)
 {
-    const int slots = std::min(p.E, p.T * p.k);
-    const dim3 g1((unsigned)ceil_div(p.I, 16), (unsigned)slots), g2((unsigned)ceil_div(p.H, 16));
-    const bool vx = p.H % 8 == 0 && ((uintptr_t)p.x & 15u) == 0;
-    if (up.format == TG_W_W4) {
-        const int gs = steps_per_scale(up.group);
-        if (vx)
-            gs == 4 ? run_up_rows<true, 4, true>(p, g1, s)
-                    : gs == 2 ? run_up_rows<true, 2, true>(p, g1, s) : run_up_rows<true, 1, true>(p, g1, s);
-        else
-            gs == 4 ? run_up_rows<true, 4, false>(p, g1, s)
-                    : gs == 2 ? run_up_rows<true, 2, false>(p, g1, s) : run_up_rows<true, 1, false>(p, g1, s);
-    } else {
-        vx ? run_up_rows<false, 4, true>(p, g1, s) : run_up_rows<false, 4, false>(p, g1, s);
-    }
+    dispatch<Up>(up, p.T, p.H, p, s);
     int st = launched("moe gate and up launch");
     if (st != TG_OK)
         return st;
-    if (down.format == TG_W_W4) {
-        const int gs = steps_per_scale(down.group);
-        gs == 4 ? run_down_rows<true, 4, true>(p, g2, s)
-                : gs == 2 ? run_down_rows<true, 2, true>(p, g2, s) : run_down_rows<true, 1, true>(p, g2, s);
-    } else {
-        p.I % 8 == 0 ? run_down_rows<false, 4, true>(p, g2, s) : run_down_rows<false, 4, false>(p, g2, s);
-    }
-    return launched("moe down launch");
+    dispatch<Down>(down, p.T, p.I, p, s);
+    if ((st = launched("moe down launch")) != TG_OK)
+        return st;
+    hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)ceil_div(p.H, 256), (unsigned)p.T), dim3(256), 0, s, p);
+    return launched("moe sum launch");
 }
 
 static ExpertStack stack_of(const tg_weight& w, int64_t K, int64_t N)
@@ -594,9 +595,10 @@ static int check_logits(const void* logits, int logits_dtype, const int32_t* ids
     return TG_OK;
 }
 
-static size_t workspace_of(int64_t T, int64_t I, int k)
+// h, then yp
+static size_t workspace_of(int64_t T, int64_t H, int64_t I, int k)
 {
-    return (size_t)std::min<int64_t>(T, kTokens) * (size_t)k * (size_t)(ceil_div(I, 16) * 16) * 4;
+    return (size_t)std::min<int64_t>(T, kTokens) * (size_t)k * (size_t)(ceil_div(I, 16) * 16 + H) * 4;
 }
 
 // everything but the choices
@@ -618,7 +620,7 @@ static int check_mlp(int64_t T, int64_t H, int64_t I, int64_t E, int k, const vo
         return st;
     if (!x || !y || (((uintptr_t)x | (uintptr_t)y) & 1u))
         return set_error(TG_E_INVAL, "x and y must be given, aligned to their elements");
-    if (!ws || ((uintptr_t)ws & 15u) || ws_bytes < workspace_of(T, I, k))
+    if (!ws || ((uintptr_t)ws & 15u) || ws_bytes < workspace_of(T, H, I, k))
         return set_error(TG_E_INVAL, "the workspace must be 16-byte aligned and hold tg_moe_workspace_bytes() bytes");
     return TG_OK;
 }
@@ -645,6 +647,7 @@ static int run_mlp(MoeParams p, int64_t T, const void* x, const int32_t* ids, co
     // passes share the workspace: the stream orders them
     for (int64_t t = 0; t < T; t += kTokens) {
         p.T = (int)std::min<int64_t>(kTokens, T - t);
+        p.yp = reinterpret_cast<float*>(p.h + (int64_t)p.T * p.k * p.stride);
         p.x = static_cast<const unsigned short*>(x) + t * p.H;
         p.ids = ids + t * p.k;
         p.weights = weights + t * p.k;
@@ -689,11 +692,11 @@ int tg_moe_route(int64_t T, int64_t E, int k, const void* logits, int dtype, int
     return launch_route(route_of(T, E, k, logits, dtype, renorm, ids, weights), current_stream());
 }
 
-int tg_moe_workspace_bytes(int64_t T, int64_t I, int k, size_t* bytes)
+int tg_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int k, size_t* bytes)
 {
-    if (!bytes || T < 0 || I < 1 || I > 65536 || k < 1 || k > kMaxChoices)
+    if (!bytes || T < 0 || H < 1 || H > 65536 || I < 1 || I > 65536 || k < 1 || k > kMaxChoices)
         return set_error(TG_E_INVAL, "bad size, or bytes is NULL");
-    *bytes = workspace_of(T, I, k);
+    *bytes = workspace_of(T, H, I, k);
     return TG_OK;
 }
 

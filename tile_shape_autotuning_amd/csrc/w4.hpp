@@ -37,11 +37,22 @@ constexpr unsigned kCodeBase = 0xC1804180u;    // -16 | 16
 constexpr unsigned kCentre = 0x41B8C1C0u;      // 23 | -24
 constexpr unsigned kOnes = 0x3F803F80u;
 
-__device__ __forceinline__ u32x4_t w4_expand(unsigned w)
+// The two constants of w4_expand, where one instruction can take them both (a
+// scalar register and a vector register: three-operand instructions hold no
+// literals), opaque to the compiler, which would fold them back into literals.
+struct CodeConsts {
+    unsigned mask, base;
+    __device__ __forceinline__ CodeConsts() : mask(kCodeMask), base(kCodeBase)
+    {
+        __asm__ __volatile__("" : "+s"(mask), "+v"(base));
+    }
+};
+
+__device__ __forceinline__ u32x4_t w4_expand(unsigned w, const CodeConsts& k)
 {
     w ^= 0xFFFF0000u;                          // complement the odd rows' codes
-    return u32x4_t{((w << 3) & kCodeMask) | kCodeBase, ((w >> 1) & kCodeMask) | kCodeBase,
-                   ((w >> 5) & kCodeMask) | kCodeBase, ((w >> 9) & kCodeMask) | kCodeBase};
+    return u32x4_t{((w << 3) & k.mask) | k.base, ((w >> 1) & k.mask) | k.base, ((w >> 5) & k.mask) | k.base,
+                   ((w >> 9) & k.mask) | k.base};
 }
 
 __device__ __forceinline__ u32x4_t splat4(unsigned v) { return u32x4_t{v, v, v, v}; }
@@ -55,29 +66,17 @@ struct W4View {
     int chunks, groups;                        // ceil(K / 128), ceil(K / group)
 };
 
-__device__ __forceinline__ float w4_scale(const W4View& v, int panel, int g, int n)
-{
-    const int64_t i = ((int64_t)panel * v.groups + g) * 16 + n;
-    if (v.scale_f32)
-        return static_cast<const float*>(v.scales)[i];
-    return __uint_as_float((unsigned)static_cast<const unsigned short*>(v.scales)[i] << 16);
-}
+// Sixteen bytes from any element address: one load, the hardware takes it unaligned.
+struct __attribute__((packed, aligned(2))) Unaligned16 {
+    u32x4_t v;
+};
 
-// 8 - zero point
-__device__ __forceinline__ float w4_shift(const W4View& v, int panel, int g, int n)
-{
-    return 8.0f - (float)v.zeros[((int64_t)panel * v.groups + g) * 16 + n];
-}
-
-// Eight bf16 at p + k (k < n counted from p); elements at and past n are zero.
-// VEC: n a multiple of 8 and p + k 16-byte aligned.
-template <bool VEC>
+// Eight bf16 at p + k; elements at and past n are zero and not read.
 __device__ __forceinline__ u32x4_t load8(const unsigned short* p, int64_t k, int64_t n)
 {
     u32x4_t v = splat4(0);
-    if constexpr (VEC) {
-        if (k < n)
-            v = *reinterpret_cast<const u32x4_t*>(p + k);
+    if (k + 8 <= n) {
+        v = reinterpret_cast<const Unaligned16*>(p + k)->v;
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -87,105 +86,19 @@ __device__ __forceinline__ u32x4_t load8(const unsigned short* p, int64_t k, int
     return v;
 }
 
-// What a lane holds of a chunk of 128 rows of NT panels: the four words of its
-// column, or four fragments of eight bf16; scales and 8 - zero point of the
-// chunk's 4 / GS groups (GS: MFMA steps of 32 rows from one scale to the next).
-template <bool W4F, int NT, int GS>
-struct PanelChunk {
-    static constexpr int SC = 4 / GS;
-    u32x4_t w[NT][W4F ? 1 : 4];
-    float s[NT][SC], d[NT][SC];
-
-    __device__ __forceinline__ void load_w4(const W4View& v, int j, int panel, int c, int lane)
-    {
-        w[j][0] = __builtin_nontemporal_load(v.words + ((int64_t)panel * v.chunks + c) * 64 + lane);
-#pragma unroll
-        for (int i = 0; i < SC; ++i) {
-            // past the last group A is zero: any finite scale of the column will do
-            const int g = min(SC == 1 ? (int)((int64_t)c * 128 / v.group) : c * SC + i, v.groups - 1);
-            s[j][i] = w4_scale(v, panel, g, lane & 15);
-            d[j][i] = v.zeros ? w4_shift(v, panel, g, lane & 15) : 0.0f;
-        }
-    }
-
-    // column `col` of a matrix stored [N][K], its K elements at p + col * K
-    template <bool VEC>
-    __device__ __forceinline__ void load_bf16(const unsigned short* p, int j, int64_t col, int c, int64_t K, int lane)
-    {
+// Four fragments: rows 128 c + 32 t + 8 kq + 0..7 of a vector of n at p.  Only
+// the last chunk of a ragged n looks at each element.
+__device__ __forceinline__ void load_chunk(u32x4_t (&f)[4], const unsigned short* p, int c, int kq, int n)
+{
+    const int k0 = c * 128;
+    if (k0 + 128 <= n) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            w[j][t] = load8<VEC>(p + col * K, (int64_t)c * 128 + 32 * t + 8 * (lane >> 4), K);
-    }
-};
-
-// total += A . W over one chunk, for the row tiles whose bit is set in `tiles`
-// (the same for the whole wave).  NA: A is the sum of NA bf16 fragments.
-template <bool W4F, int MT, int NT, int NA, int GS>
-__device__ __forceinline__ void mac_chunk(f32x4_t (&total)[MT][NT], const u32x4_t (&a)[MT][NA][4],
-                                          const PanelChunk<W4F, NT, GS>& b, bool zero, unsigned tiles)
-{
-    const f32x4_t none = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (W4F) {
-        f32x4_t acc[MT][NT], mid[MT], sum[MT];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (t % GS == 0) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mid[m] = sum[m] = none;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[m][j] = none;
-                }
-            }
-            u32x4_t q[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                q[j] = w4_expand(b.w[j][0][t]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (!(tiles >> m & 1))
-                    continue;
-#pragma unroll
-                for (int n = 0; n < NA; ++n) {
-                    mid[m] = mfma_bf16(a[m][n][t], splat4(kCentre), mid[m]);
-                    if (zero)
-                        sum[m] = mfma_bf16(a[m][n][t], splat4(kOnes), sum[m]);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[m][j] = mfma_bf16(a[m][n][t], q[j], acc[m][j]);
-                }
-            }
-            if (t % GS == GS - 1) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (!(tiles >> m & 1))
-                        continue;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            float v = acc[m][j][r] + mid[m][r];
-                            if (zero)
-                                v = fmaf(b.d[j][t / GS], sum[m][r], v);
-                            total[m][j][r] = fmaf(b.s[j][t / GS], v, total[m][j][r]);
-                        }
-                }
-            }
-        }
+            f[t] = reinterpret_cast<const Unaligned16*>(p + k0 + 32 * t + 8 * kq)->v;
     } else {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (!(tiles >> m & 1))
-                    continue;
-#pragma unroll
-                for (int n = 0; n < NA; ++n)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        total[m][j] = mfma_bf16(a[m][n][t], b.w[j][t], total[m][j]);
-            }
+            f[t] = load8(p, k0 + 32 * t + 8 * kq, n);
     }
 }
 

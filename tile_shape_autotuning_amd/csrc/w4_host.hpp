@@ -8,6 +8,9 @@
 
 namespace tg {
 
+constexpr size_t kLdsBytes = 160 * 1024;       // of a workgroup on gfx950
+constexpr int kCus = 256;
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // TG_OK, or the error (set) for a K x N weight of `w`'s format.

@@ -211,7 +211,7 @@ def _experts(x, gate_up, down, E, k, gate, out):
         out = torch.empty_like(x)
     elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous() or out.device != x.device:
         raise ValueError("out must be a contiguous bfloat16 tensor shaped like x")
-    ws = torch.empty(_native.moe_workspace_bytes(T, inter, k), dtype=torch.uint8, device=x.device)
+    ws = torch.empty(_native.moe_workspace_bytes(T, H, inter, k), dtype=torch.uint8, device=x.device)
     return T, H, inter, n, up, dn, out, ws
 
 
