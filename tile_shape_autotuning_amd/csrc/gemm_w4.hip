@@ -6,7 +6,9 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
+#include "kernels/gemm_tiled_dma.hpp"
 #include "panel_stream.hpp"
 #include "w4.hpp"
 #include "w4_host.hpp"
@@ -120,6 +122,231 @@ static int launch_panels(GemmW4Params p, int per, hipStream_t s)
     return launched("gemm_w4 launch");
 }
 
+// Many rows: a workgroup's four waves stand side by side over 64 NT columns and
+// share MT x 16 rows of A, whose chunks of 128 k arrive in LDS (16-byte
+// transfers straight from memory, three stages).  W's codes are a quarter of
+// A's bytes, so tiles are wide rather than tall, and no two waves expand the
+// same codes: with NT = 4 and MT = 8, 144 expanding instructions a chunk beside
+// 128 MFMAs and 128 FMAs of the scales.  The sums that do not depend on the
+// column (w4.hpp) are computed one chunk ahead, each wave a quarter of the
+// rows, and start the accumulators.  One barrier a chunk.
+//
+// Stage layout: row r of A, 256 bytes, 16-byte piece q at q ^ swz<16>(r): the
+// 16 rows of a fragment read hit 16 different pieces.
+template <bool ZERO, int MT, int NT, int GS>
+struct TiledW4 {
+    static constexpr int BM = 16 * MT, SC = 4 / GS, STAGE = BM * 256, STAGES = 3;
+    static constexpr int MIDS = SC * MT * 4 * (ZERO ? 2 : 1);          // f32x4, held twice
+    static constexpr int LDS = STAGES * STAGE + 2 * MIDS * 16;
+};
+
+template <bool ZERO, int MT, int NT, int GS, bool VEC>
+__global__ void __launch_bounds__(256) gemm_w4_tiled_kernel(GemmW4Params p)
+{
+    using T = TiledW4<ZERO, MT, NT, GS>;
+    constexpr int SC = T::SC, BM = T::BM;
+    extern __shared__ u32x4_t lds[];
+    f32x4_t* mids = reinterpret_cast<f32x4_t*>(lds + T::STAGES * T::STAGE / 16);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l16 = lane & 15, kq = lane >> 4;
+    const int tiles_n = (p.panels + 4 * NT - 1) / (4 * NT), tiles_m = (int)((p.M + BM - 1) / BM);
+    int tile, tm, tn, split;
+    map_block(blockIdx.x, gridDim.x, tiles_m, tiles_n, 8, tile, tm, tn, split);
+    const int64_t row0 = (int64_t)tm * BM;
+    const int panel0 = (tn * 4 + wave) * NT;
+    const int K = (int)p.K, chunks = p.w.chunks;
+    const int rows = (int)min((int64_t)BM, p.M - row0);
+    const unsigned short* A = p.A + row0 * K;
+    const CodeConsts code;
+    const unsigned up = p.w.scale_f32 || (lane & 1) ? 0 : 16, keep = p.w.scale_f32 ? ~0u : 0xFFFF0000u;
+
+    // A's chunk c into its stage: transfer j brings rows 4 j .. 4 j + 3
+    const i32x4_t ra = rsrc_words(A, (int64_t)rows * K * 2);
+    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    auto fetch = [&](int c) {
+        const unsigned base = c % T::STAGES * T::STAGE;
+#pragma unroll
+        for (int q = 0; q < BM / 16; ++q) {
+            const int j = q * 4 + wave, row = 4 * j + kq;
+            const int k = c * 128 + (l16 ^ swz<16>(row)) * 8;
+            if constexpr (VEC) {
+                dma16(ra, row < rows && k < K ? (row * K + k) * 2 : kOOB, lds0 + base + j * 1024);
+            } else {
+                u32x4_t v = splat4(0);
+                if (row < rows)
+                    v = load8(A + (int64_t)row * K, k, K);
+                lds[base / 16 + j * 64 + lane] = v;
+            }
+        }
+    };
+    auto fragment = [&](int c, int m, int t) {
+        const int row = 16 * m + l16;
+        return lds[c % T::STAGES * (T::STAGE / 16) + row * 16 + ((4 * t + kq) ^ swz<16>(row))];
+    };
+    // the constant sums of chunk c: this wave's quarter of the rows
+    auto correct = [&](int c) {
+        f32x4_t* to = mids + (c & 1) * T::MIDS;
+        const f32x4_t none = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < MT / 4; ++h) {
+            const int m = wave * (MT / 4) + h;
+#pragma unroll
+            for (int q = 0; q < SC; ++q) {
+                f32x4_t v = none, s = none;
+#pragma unroll
+                for (int t = q * GS; t < (q + 1) * GS; ++t) {
+                    const u32x4_t a = fragment(c, m, t);
+                    v = mfma_bf16(a, splat4(kCentre), v);
+                    if constexpr (ZERO)
+                        s = mfma_bf16(a, splat4(kOnes), s);
+                }
+                if (l16 == 0) {
+                    to[(q * MT + m) * 4 + kq] = v;
+                    if constexpr (ZERO)
+                        to[(SC * MT + q * MT + m) * 4 + kq] = s;
+                }
+            }
+        }
+    };
+    struct Words {
+        u32x4_t w[NT];
+        unsigned s[NT][SC];
+        unsigned char z[NT][ZERO ? SC : 1];
+    };
+    auto load = [&](int c, Words& b) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int panel = panel0 + j;
+            const bool some = panel < p.panels && c < chunks;
+            const __amdgpu_buffer_rsrc_t rw =
+                make_rsrc(p.w.words + (int64_t)panel * chunks * 64, some ? (int64_t)chunks * 1024 : 0);
+            const int64_t per = (int64_t)panel * p.w.groups * 16;
+            const int n = some ? p.w.groups * 16 : 0;
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(
+                static_cast<const char*>(p.w.scales) + per * (p.w.scale_f32 ? 4 : 2), n * (p.w.scale_f32 ? 4 : 2));
+            const __amdgpu_buffer_rsrc_t rz = make_rsrc(p.w.zeros + (ZERO ? per : 0), n);
+            b.w[j] = load16(rw, c * 1024 + lane * 16);
+#pragma unroll
+            for (int q = 0; q < SC; ++q) {
+                const int at = (int)((unsigned)(c * 128 + 32 * GS * q) / (unsigned)p.w.group) * 16 + l16;
+                b.s[j][q] = load4(rs, p.w.scale_f32 ? at * 4 : at / 2 * 4);
+                if constexpr (ZERO)
+                    b.z[j][q] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
+            }
+        }
+    };
+
+    f32x4_t total[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            total[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    auto multiply = [&](int c, const Words& b) {
+        const f32x4_t* from = mids + (c & 1) * T::MIDS;
+        f32x4_t acc[MT][NT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int q = t / GS;
+            u32x4_t w[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                w[j] = w4_expand(b.w[j][t], code);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const u32x4_t a = fragment(c, m, t);
+                if (t % GS == 0) {
+                    const f32x4_t v = from[(q * MT + m) * 4 + kq];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        acc[m][j] = v;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[m][j] = mfma_bf16(a, w[j], acc[m][j]);
+            }
+            if (t % GS == GS - 1) {
+                float scale[NT], d[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    scale[j] = __uint_as_float((b.s[j][q] << up) & keep);
+                    if constexpr (ZERO)
+                        d[j] = 8.0f - (float)b.z[j][q];
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    f32x4_t s;
+                    if constexpr (ZERO)
+                        s = from[(SC * MT + q * MT + m) * 4 + kq];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            total[m][j][r] =
+                                fmaf(scale[j], ZERO ? fmaf(d[j], s[r], acc[m][j][r]) : acc[m][j][r], total[m][j][r]);
+                }
+            }
+        }
+    };
+
+    Words b[2];
+    load(0, b[0]);
+    fetch(0);
+    fetch(1);
+    wait_vm_all();
+    lds_barrier();
+    correct(0);
+    // the transfers are not the compiler's to wait for: every chunk waits for
+    // all that is on its way, A's chunk c + 1 and the words of chunk c, both
+    // asked for a whole chunk ago
+    auto one = [&](int c, const Words& now, Words& next) {
+        wait_vm_all();
+        lds_barrier();
+        load(c + 1, next);
+        fetch(c + 2);
+        correct(c + 1);
+        multiply(c, now);
+        return c + 1 < chunks;
+    };
+    for (int c = 0;; c += 2)
+        if (!one(c, b[0], b[1]) || !one(c + 1, b[1], b[0]))
+            break;
+    // nothing may still be writing LDS when the workgroup ends
+    wait_vm_all();
+
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            store_tile(p, row0 + 16 * m, (int64_t)(panel0 + j) * 16, total[m][j], lane);
+}
+
+template <int MT, int NT>
+static int launch_tiled(const GemmW4Params& p, hipStream_t s)
+{
+    const bool vec = p.K % 8 == 0 && ((uintptr_t)p.A & 15u) == 0;
+    const dim3 grid((unsigned)(ceil_div(p.panels, 4 * NT) * ceil_div(p.M, 16 * MT))), block(256);
+    auto go = [&](auto zero, auto gs) {
+        constexpr bool Z = decltype(zero)::value;
+        constexpr int G = decltype(gs)::value;
+        constexpr size_t lds = TiledW4<Z, MT, NT, G>::LDS;
+        if (vec)
+            hipLaunchKernelGGL((gemm_w4_tiled_kernel<Z, MT, NT, G, true>), grid, block, lds, s, p);
+        else
+            hipLaunchKernelGGL((gemm_w4_tiled_kernel<Z, MT, NT, G, false>), grid, block, lds, s, p);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Four = std::integral_constant<int, 4>;
+    auto pick = [&](auto zero) {
+        p.w.group >= 128 ? go(zero, Four{}) : p.w.group == 64 ? go(zero, Two{}) : go(zero, One{});
+    };
+    p.w.zeros ? pick(std::true_type{}) : pick(std::false_type{});
+    return launched("gemm_w4 launch");
+}
+
 }  // namespace tg
 
 using namespace tg;
@@ -168,5 +395,9 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
         return p.w.chunks <= 16 ? launch_panels<1, 16, 1>(p, per, s) : launch_panels<1, 16, 2>(p, per, s);
     if (M <= 32)
         return launch_panels<2, 16, 1>(p, per, s);
-    return launch_panels<4, 8, 2>(p, per, s);
+    if (M <= 64)
+        return launch_panels<4, 8, 2>(p, per, s);
+    if (ceil_div(M, 128) * ceil_div(p.panels, 16) >= kCus)
+        return launch_tiled<8, 4>(p, s);
+    return launch_tiled<4, 2>(p, s);
 }
