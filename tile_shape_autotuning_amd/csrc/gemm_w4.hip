@@ -126,10 +126,13 @@ static int launch_panels(GemmW4Params p, int per, hipStream_t s)
 // share MT x 16 rows of A, whose chunks of 128 k arrive in LDS (16-byte
 // transfers straight from memory, three stages).  W's codes are a quarter of
 // A's bytes, so tiles are wide rather than tall, and no two waves expand the
-// same codes: with NT = 4 and MT = 8, 144 expanding instructions a chunk beside
-// 128 MFMAs and 128 FMAs of the scales.  The sums that do not depend on the
-// column (w4.hpp) are computed one chunk ahead, each wave a quarter of the
-// rows, and start the accumulators.  One barrier a chunk.
+// same codes: with MT = NT = 4, 144 expanding instructions a chunk beside 64
+// MFMAs and 64 FMAs of the scales.  The sums that do not depend on the column
+// (w4.hpp) are computed one chunk ahead, each wave a quarter of the rows, and
+// start the accumulators.  One barrier a chunk; it and the transfers are
+// covered by the other workgroups of the compute unit (two of 256 registers
+// with NT = 4, three with NT = 2).  Bound by issue: 2048 x 4096 x 4096 77 us, 0.9
+// PFLOP/s; 4096 x 8192 x 8192 525 us, 1.05 PFLOP/s.
 //
 // Stage layout: row r of A, 256 bytes, 16-byte piece q at q ^ swz<16>(r): the
 // 16 rows of a fragment read hit 16 different pieces.
@@ -141,7 +144,8 @@ struct TiledW4 {
 };
 
 template <bool ZERO, int MT, int NT, int GS, bool VEC>
-__global__ void __launch_bounds__(256) gemm_w4_tiled_kernel(GemmW4Params p)
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NT == 1 ? 4 : NT == 2 ? 3 : 2)))
+gemm_w4_tiled_kernel(GemmW4Params p)
 {
     using T = TiledW4<ZERO, MT, NT, GS>;
     constexpr int SC = T::SC, BM = T::BM;
@@ -397,7 +401,13 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
         return launch_panels<2, 16, 1>(p, per, s);
     if (M <= 64)
         return launch_panels<4, 8, 2>(p, per, s);
-    if (ceil_div(M, 128) * ceil_div(p.panels, 16) >= kCus)
-        return launch_tiled<8, 4>(p, s);
-    return launch_tiled<4, 2>(p, s);
+    // 64 x 256 tiles where two workgroups a compute unit have one, 64 x 128 where
+    // one has, else 64 x 64: 2048 x 4096 x 4096 77, 85 and 112 us, 100 x 28672 x
+    // 4096 59, 50 and 66, 128 x 4096 x 4096 58, 38 and 30.  (128 x 256 leaves
+    // one workgroup a compute unit: 151 us for the first.)
+    if (ceil_div(M, 64) * ceil_div(p.panels, 16) >= 2 * kCus)
+        return launch_tiled<4, 4>(p, s);
+    if (ceil_div(M, 64) * ceil_div(p.panels, 8) >= kCus)
+        return launch_tiled<4, 2>(p, s);
+    return launch_tiled<4, 1>(p, s);
 }

@@ -9,17 +9,19 @@
 // rounded as if exact (ties to even): rint of a float estimate, corrected by
 // the sign of the remainder that one FMA gives exactly.
 //
-// One 256-thread workgroup takes 64 columns (four panels, one a wave) and one
-// group of rows, or 128 rows when groups are smaller.  Each chunk of 128 rows
-// goes through LDS, so that global reads and writes follow the input's own
-// order (either may be contiguous) and a lane then holds the 32 elements of
-// its four words.  Lanes l, l + 16, l + 32, l + 48 share a column: a group's
-// extremes are a maximum over a lane's own elements and two shuffles.  Groups
-// of more than 128 rows are read twice, first for the extremes.
+// A wave takes 16 columns (a panel) and one group of rows, or 128 rows when
+// groups are smaller; a workgroup's four waves take neighbouring panels.  A lane
+// holds the 32 elements of its four words; lanes l, l + 16, l + 32 and l + 48
+// share a column, so a group's extremes are those of a lane's own elements and
+// two shuffles.  A matrix stored [N][K] has a lane's eight rows contiguous and
+// is read straight into registers, and its values written back the same way; one
+// stored [K][N] crosses LDS, which turns rows of 64 columns into columns.
+// Groups of more than 128 rows are read twice, first for the extremes.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "w4.hpp"
 #include "w4_host.hpp"
@@ -38,122 +40,179 @@ struct QuantParams {
 
 static constexpr int kQCols = 64, kQRows = 128;
 
-// rint(w * inv) made rint(w / s) for finite w and normal s > 0: the remainder
-// against the two neighbouring half steps has its exact sign.
-__device__ __forceinline__ float rint_quotient(float w, float s, float inv)
+// rint(w / s) for finite w and normal s > 0, q = rint(w * inv) given: the
+// remainder against the two neighbouring half steps has its exact sign.
+__device__ __forceinline__ float exact_quotient(float w, float s, float q)
 {
-    float q = rintf(w * inv);
     const float up = fmaf(-(q + 0.5f), s, w), down = fmaf(-(q - 0.5f), s, w);
     const bool odd = ((int)q & 1) != 0;
     if (up > 0.0f || (up == 0.0f && odd))
-        q += 1.0f;
-    else if (down < 0.0f || (down == 0.0f && odd))
-        q -= 1.0f;
+        return q + 1.0f;
+    if (down < 0.0f || (down == 0.0f && odd))
+        return q - 1.0f;
     return q;
 }
 
-template <bool BF16, bool ROWS>
+// VEC: sixteen bytes at a time along the matrix's contiguous dimension.
+template <bool BF16, bool ROWS, bool VEC>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(QuantParams p)
 {
-    __shared__ float tile[kQRows * (kQCols + 1)];
+    // row r of the tile at r * STRIDE bytes: lanes 16 apart, eight rows, fall on other banks
+    constexpr int EB = BF16 ? 2 : 4, STRIDE = kQCols * EB + 8;
+    __shared__ __align__(16) char tile[ROWS ? kQRows * STRIDE : 16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = lane & 15, kq = lane >> 4;
     const int col0 = blockIdx.x * kQCols;
-    const int panel = blockIdx.x * (kQCols / 16) + wave;
+    const int panel = blockIdx.x * (kQCols / 16) + wave, col = panel * 16 + n;
     const int64_t mat = blockIdx.z;
     const int span = max(p.group, kQRows);             // rows of this workgroup
     const int64_t row_first = (int64_t)blockIdx.y * span;
     const int nch = (int)((min((int64_t)p.K, row_first + span) - row_first + kQRows - 1) / kQRows);
-    const int64_t base = mat * (int64_t)p.K * p.N;
+    const char* W = static_cast<const char*>(p.W) + mat * (int64_t)p.K * p.N * EB;
+    char* V = static_cast<char*>(p.values) + (p.values ? mat * (int64_t)p.K * p.N * EB : 0);
 
-    auto load = [&](int64_t r0) {
-        __syncthreads();
-        for (int i = tid; i < kQRows * kQCols; i += 256) {
-            const int r = ROWS ? i / kQCols : i % kQRows, c = ROWS ? i % kQCols : i / kQRows;
-            float v = 0.0f;
-            if (r0 + r < p.K && col0 + c < p.N) {
-                const int64_t at = base + (ROWS ? (r0 + r) * p.N + col0 + c : (int64_t)(col0 + c) * p.K + r0 + r);
-                v = BF16 ? __uint_as_float((unsigned)static_cast<const unsigned short*>(p.W)[at] << 16)
-                         : static_cast<const float*>(p.W)[at];
-            }
-            tile[r * (kQCols + 1) + c] = v;
-        }
-        __syncthreads();
+    auto element = [](const char* at) {
+        if constexpr (BF16)
+            return __uint_as_float((unsigned)*reinterpret_cast<const unsigned short*>(at) << 16);
+        else
+            return *reinterpret_cast<const float*>(at);
     };
+    auto put = [](char* at, float x) {
+        if constexpr (BF16)
+            *reinterpret_cast<unsigned short*>(at) = f32_to_bf16_rne(x);
+        else
+            *reinterpret_cast<float*>(at) = x;
+    };
+    // pieces of 16 bytes of the tile's rows (ROWS), eight bytes aligned in LDS
+    constexpr int PIECES = kQCols * EB / 16;
+    auto piece = [&](int i, int& r, int& c) {
+        r = i / PIECES;
+        c = i % PIECES * (16 / EB);
+    };
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
     float v[4][8];
-    auto take = [&] {
+    auto load = [&](int64_t r0) {
+        if constexpr (ROWS) {
+            __syncthreads();
+            for (int i = tid; i < kQRows * PIECES; i += 256) {
+                int r, c;
+                piece(i, r, c);
+                char* to = tile + r * STRIDE + c * EB;
+                const char* from = W + ((r0 + r) * p.N + col0 + c) * EB;
+                u32x4_t x = splat4(0);
+                if constexpr (VEC) {
+                    if (r0 + r < p.K && col0 + c < p.N)
+                        x = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from));
+                } else {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+                    for (int e = 0; e < 16 / EB; ++e)
+                        if (r0 + r < p.K && col0 + c + e < p.N) {
+                            if constexpr (BF16)
+                                x[e >> 1] |= (unsigned)reinterpret_cast<const unsigned short*>(from)[e]
+                                             << (16 * (e & 1));
+                            else
+                                x[e & 3] = reinterpret_cast<const unsigned*>(from)[e];
+                        }
+                }
+                reinterpret_cast<u32x2*>(to)[0] = u32x2{x[0], x[1]};
+                reinterpret_cast<u32x2*>(to)[1] = u32x2{x[2], x[3]};
+            }
+            __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[t][e] = tile[(32 * t + 8 * kq + e) * (kQCols + 1) + wave * 16 + n];
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[t][e] = element(tile + (32 * t + 8 * kq + e) * STRIDE + (wave * 16 + n) * EB);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int64_t k = r0 + 32 * t + 8 * kq;
+                const char* from = W + ((int64_t)col * p.K + k) * EB;
+                if constexpr (VEC) {
+                    constexpr int X = EB / 2;          // 16-byte loads
+                    u32x4_t x[X];
+#pragma unroll
+                    for (int q = 0; q < X; ++q)
+                        x[q] = col < p.N && k + q * 4 < p.K
+                                   ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from) + q)
+                                   : splat4(0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if constexpr (BF16)
+                            v[t][e] = __uint_as_float(e & 1 ? x[0][e >> 1] & 0xFFFF0000u : x[0][e >> 1] << 16);
+                        else
+                            v[t][e] = __uint_as_float(x[e >> 2][e & 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[t][e] = col < p.N && k + e < p.K ? element(from + e * EB) : 0.0f;
+                }
+            }
+        }
     };
-    // extremes of this lane's four runs of eight; `bad`: something not finite
+    // extremes of this lane's four runs of eight; size: of the magnitudes, as
+    // bits, which order infinities and NaN last
     float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
-    int bad[4] = {0, 0, 0, 0};
-    auto widen = [&] {
+    unsigned size[4] = {0, 0, 0, 0};
+    for (int c = 0; c < nch; ++c) {
+        load(row_first + (int64_t)c * kQRows);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                lo[t] = fminf(lo[t], v[t][e]);
-                hi[t] = fmaxf(hi[t], v[t][e]);
-                bad[t] |= !(fabsf(v[t][e]) < INFINITY);
+                size[t] = max(size[t], __float_as_uint(v[t][e]) & 0x7FFFFFFFu);
+                if (p.zero) {
+                    lo[t] = fminf(lo[t], v[t][e]);
+                    hi[t] = fmaxf(hi[t], v[t][e]);
+                }
             }
-    };
-    for (int c = 0; c < nch; ++c) {
-        load(row_first + (int64_t)c * kQRows);
-        take();
-        widen();
     }
+    auto join = [&](int t, float l, float h, unsigned z) {
+        lo[t] = fminf(lo[t], l);
+        hi[t] = fmaxf(hi[t], h);
+        size[t] = max(size[t], z);
+    };
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int off = 16; off <= 32; off <<= 1) {
-            lo[t] = fminf(lo[t], __shfl_xor(lo[t], off));
-            hi[t] = fmaxf(hi[t], __shfl_xor(hi[t], off));
-            bad[t] |= __shfl_xor(bad[t], off);
-        }
+        for (int off = 16; off <= 32; off <<= 1)
+            join(t, __shfl_xor(lo[t], off), __shfl_xor(hi[t], off), (unsigned)__shfl_xor((int)size[t], off));
     if (p.group >= 64)
 #pragma unroll
         for (int t = 0; t < 4; t += 2) {
-            lo[t] = lo[t + 1] = fminf(lo[t], lo[t + 1]);
-            hi[t] = hi[t + 1] = fmaxf(hi[t], hi[t + 1]);
-            bad[t] = bad[t + 1] = bad[t] | bad[t + 1];
+            join(t, lo[t + 1], hi[t + 1], size[t + 1]);
+            join(t + 1, lo[t], hi[t], size[t]);
         }
-    if (p.group >= 128) {
-        const float l = fminf(lo[0], lo[2]), h = fmaxf(hi[0], hi[2]);
-        const int b = bad[0] | bad[2];
+    if (p.group >= 128)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            lo[t] = l;
-            hi[t] = h;
-            bad[t] = b;
-        }
-    }
+        for (int t = 0; t < 4; ++t)
+            join(t, lo[t ^ 2], hi[t ^ 2], size[t ^ 2]);
 
     // quotients are taken of w * up and s * up: up = 2^64 keeps the remainders
     // of groups near the smallest normal number from vanishing
     float s[4], z[4], inv[4], up[4], su[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        s[t] = p.zero ? (hi[t] - lo[t]) / 15.0f : fmaxf(hi[t], -lo[t]) / 7.0f;
+        const bool bad = size[t] >= 0x7F800000u;
+        s[t] = p.zero ? (hi[t] - lo[t]) / 15.0f : __uint_as_float(size[t]) / 7.0f;
         if (!p.scale_f32)
             s[t] = __uint_as_float((unsigned)f32_to_bf16_rne(s[t]) << 16);
-        const bool usable = !bad[t] && s[t] > 0.0f && s[t] < INFINITY;
+        const bool usable = !bad && s[t] > 0.0f && s[t] < INFINITY;
         up[t] = s[t] < 0x1p-80f ? 0x1p64f : 1.0f;
         su[t] = s[t] * up[t];
         inv[t] = usable ? 1.0f / su[t] : 0.0f;
         z[t] = 8.0f;
         if (p.zero)
-            z[t] = usable ? fminf(rint_quotient(-lo[t] * up[t], su[t], inv[t]), 15.0f) : 0.0f;
-        if (bad[t])
+            z[t] = usable ? fminf(exact_quotient(-lo[t] * up[t], su[t], rintf(-lo[t] * up[t] * inv[t])), 15.0f) : 0.0f;
+        if (bad)
             s[t] = NAN;
     }
     // scales and zero points: one lane a column and group; columns past N hold zero
     if (kq == 0 && panel < p.panels) {
         const int per = p.group >= 128 ? 4 : p.group / 32;     // runs of 32 rows in a group
-        const bool real = panel * 16 + n < p.N;
+        const bool real = col < p.N;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int64_t g = (row_first + 32 * t) / p.group;
@@ -171,45 +230,97 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(QuantParams p)
 
     for (int c = 0; c < nch; ++c) {
         const int64_t r0 = row_first + (int64_t)c * kQRows;
-        if (nch > 1) {
+        if (nch > 1)
             load(r0);
-            take();
-        }
         u32x4_t w;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
+            float q[8], off = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = v[t][e] * up[t] * inv[t];
+                q[e] = rintf(x);
+                off = fmaxf(off, fabsf(x - q[e]));
+            }
+            // x is off by less than 2^-18: only a quotient that near to the
+            // middle of two codes can have been rounded to the wrong one
+            if (off > 0.5f - 0x1p-18f && inv[t] != 0.0f)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    q[e] = exact_quotient(v[t][e] * up[t], su[t], q[e]);
             unsigned word = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float q = z[t];
-                if (inv[t] != 0.0f)
-                    q = fminf(fmaxf(rint_quotient(v[t][e] * up[t], su[t], inv[t]) + z[t], 0.0f), 15.0f);
-                const bool real = r0 + 32 * t + 8 * kq + e < p.K && panel * 16 + n < p.N;
-                word |= (real ? (unsigned)q : 0u) << (4 * (e >> 1) + 16 * (e & 1));
-                v[t][e] = (q - z[t]) * s[t];
+                float code = fminf(fmaxf(q[e] + z[t], 0.0f), 15.0f);
+                if (inv[t] == 0.0f)
+                    code = z[t];
+                word |= (unsigned)code << (4 * (e >> 1) + 16 * (e & 1));
+                v[t][e] = (code - z[t]) * s[t];
             }
+            // nothing is stored past K and N
+            const int64_t left = p.K - (r0 + 32 * t + 8 * kq);
+            if (left < 8 || col >= p.N)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e >= left || col >= p.N)
+                        word &= ~(15u << (4 * (e >> 1) + 16 * (e & 1)));
             w[t] = word;
         }
         if (panel < p.panels)
-            p.words[((mat * p.panels + panel) * p.chunks + r0 / kQRows) * 64 + lane] = w;
-        if (p.values) {
+            __builtin_nontemporal_store(w, p.words + ((mat * p.panels + panel) * p.chunks + r0 / kQRows) * 64 + lane);
+        if (!p.values)
+            continue;
+        if constexpr (ROWS) {
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    tile[(32 * t + 8 * kq + e) * (kQCols + 1) + wave * 16 + n] = v[t][e];
+                    put(tile + (32 * t + 8 * kq + e) * STRIDE + (wave * 16 + n) * EB, v[t][e]);
             __syncthreads();
-            for (int i = tid; i < kQRows * kQCols; i += 256) {
-                const int r = ROWS ? i / kQCols : i % kQRows, cc = ROWS ? i % kQCols : i / kQRows;
-                if (r0 + r >= p.K || col0 + cc >= p.N)
-                    continue;
-                const int64_t at = base + (ROWS ? (r0 + r) * p.N + col0 + cc : (int64_t)(col0 + cc) * p.K + r0 + r);
-                const float x = tile[r * (kQCols + 1) + cc];
-                if (BF16)
-                    static_cast<unsigned short*>(p.values)[at] = f32_to_bf16_rne(x);
-                else
-                    static_cast<float*>(p.values)[at] = x;
+            for (int i = tid; i < kQRows * PIECES; i += 256) {
+                int r, cc;
+                piece(i, r, cc);
+                const char* from = tile + r * STRIDE + cc * EB;
+                char* to = V + ((r0 + r) * p.N + col0 + cc) * EB;
+                if constexpr (VEC) {
+                    const u32x2 a = reinterpret_cast<const u32x2*>(from)[0], b = reinterpret_cast<const u32x2*>(from)[1];
+                    if (r0 + r < p.K && col0 + cc < p.N)
+                        __builtin_nontemporal_store(u32x4_t{a[0], a[1], b[0], b[1]}, reinterpret_cast<u32x4_t*>(to));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16 / EB; ++e)
+                        if (r0 + r < p.K && col0 + cc + e < p.N)
+                            put(to + e * EB, element(from + e * EB));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int64_t k = r0 + 32 * t + 8 * kq;
+                char* to = V + ((int64_t)col * p.K + k) * EB;
+                if constexpr (VEC) {
+                    constexpr int X = EB / 2;
+                    u32x4_t x[X];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if constexpr (BF16) {
+                            const unsigned h = f32_to_bf16_rne(v[t][e]);
+                            x[0][e >> 1] = e & 1 ? x[0][e >> 1] | h << 16 : h;
+                        } else {
+                            x[e >> 2][e & 3] = __float_as_uint(v[t][e]);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < X; ++q)
+                        if (col < p.N && k + q * 4 < p.K)
+                            __builtin_nontemporal_store(x[q], reinterpret_cast<u32x4_t*>(to) + q);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (col < p.N && k + e < p.K)
+                            put(to + e * EB, v[t][e]);
+                }
             }
         }
     }
@@ -284,16 +395,16 @@ extern "C" int tg_w4_quantize(int64_t count, int64_t K, int64_t N, int group, co
     p.zero = zeros != nullptr;
     const dim3 grid((unsigned)ceil_div(N, kQCols), (unsigned)ceil_div(K, span), (unsigned)count);
     hipStream_t s = current_stream();
-    if (dtype == TG_BF16) {
-        if (rows_first)
-            hipLaunchKernelGGL((w4_quantize_kernel<true, true>), grid, dim3(256), 0, s, p);
+    const int64_t run = rows_first ? N : K;            // contiguous elements
+    const bool vec = run % (dtype == TG_BF16 ? 8 : 4) == 0 && (((uintptr_t)W | (uintptr_t)values) & 15u) == 0;
+    auto go = [&](auto bf16, auto rows) {
+        constexpr bool B = decltype(bf16)::value, R = decltype(rows)::value;
+        if (vec)
+            hipLaunchKernelGGL((w4_quantize_kernel<B, R, true>), grid, dim3(256), 0, s, p);
         else
-            hipLaunchKernelGGL((w4_quantize_kernel<true, false>), grid, dim3(256), 0, s, p);
-    } else {
-        if (rows_first)
-            hipLaunchKernelGGL((w4_quantize_kernel<false, true>), grid, dim3(256), 0, s, p);
-        else
-            hipLaunchKernelGGL((w4_quantize_kernel<false, false>), grid, dim3(256), 0, s, p);
-    }
+            hipLaunchKernelGGL((w4_quantize_kernel<B, R, false>), grid, dim3(256), 0, s, p);
+    };
+    auto pick = [&](auto bf16) { rows_first ? go(bf16, std::true_type{}) : go(bf16, std::false_type{}); };
+    dtype == TG_BF16 ? pick(std::true_type{}) : pick(std::false_type{});
     return launched("w4_quantize launch");
 }
