@@ -47,8 +47,8 @@ HEADERS = [os.path.join(CSRC, f) for f in ("select.hpp", "registry.hpp", "runtim
 
 
 # headers of the 4-bit weight and expert kernels only
-W4_HEADERS = [os.path.join(CSRC, f) for f in ("w4.hpp", "w4_host.hpp")]
-W4_SOURCES = ("w4_quantize.hip", "gemm_w4.hip", "moe.hip")
+W4_HEADERS = [os.path.join(CSRC, f) for f in ("w4.hpp", "w4_host.hpp", "panel_stream.hpp", "moe.hpp")]
+W4_SOURCES = ("w4_quantize.hip", "gemm_w4.hip", "moe.hip", "moe_up.hip", "moe_down.hip")
 
 
 def kernel_source_digest() -> str:

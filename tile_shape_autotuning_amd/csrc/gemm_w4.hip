@@ -51,49 +51,70 @@ template <int MT>
 constexpr int kHalf = MT == 4 ? 32 : 64;
 
 // A workgroup multiplies MT x 16 rows with p.per panels (panel_stream.hpp).  K
-// beyond the waves' W x CW chunks comes in further blocks, whose sums wait in
-// LDS.
-template <bool ZERO, int MT, int W, int CW, int GS>
+// beyond the waves' W x CW chunks comes in further blocks; with more than one
+// panel (!ONE) the sums of the earlier blocks wait in LDS.
+template <bool ZERO, int MT, int W, int CW, int GS, bool VEC, bool ONE>
 __global__ void __launch_bounds__(64 * W) gemm_w4_panels_kernel(GemmW4Params p)
 {
-    using S = PanelStream<true, ZERO, MT, 1, 1, W, CW, GS, kHalf<MT>>;
+    using S = PanelStream<true, ZERO, MT, 1, 1, W, CW, GS, ONE ? 1 : kHalf<MT>>;
     __shared__ f32x4_t red[S::RED], mid[S::MID];
-    extern __shared__ f32x4_t part[];                  // [p.per][MT][64] if there is more than one block
+    extern __shared__ f32x4_t part[];                  // [p.per][MT][64] if it is used
     S s(red, mid, p.w.scale_f32);
-    const int lane = s.lane, l16 = lane & 15, kq = lane >> 4;
+    const int lane = s.lane, l16 = lane & 15;
     const int panel0 = blockIdx.x * p.per;
     const int n = min(p.per, p.panels - panel0);
     const int64_t row0 = (int64_t)blockIdx.y * (16 * MT);
-    const int K = (int)p.K;
+    const int K = (int)p.K, here = (int)min((int64_t)(16 * MT), p.M - row0);
+    const unsigned short* A = p.A + row0 * K;
 
-    auto rows = [&](int block) {
+    auto rows = [&](int block, typename S::Rows& x, bool some) {
         const int c0 = (block * W + s.wave) * CW;
+        const __amdgpu_buffer_rsrc_t r = wave_rsrc(A, some ? (int64_t)here * K * 2 : 0);
 #pragma unroll
-        for (int i = 0; i < CW; ++i)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    s.a[i][m][0][t] = splat4(0);
-                const int64_t row = row0 + 16 * m + l16;
-                if (c0 + i < p.w.chunks && row < p.M)
-                    load_chunk(s.a[i][m][0], p.A + row * p.K, c0 + i, kq, K);
-            }
+        for (int m = 0; m < MT; ++m) {
+            const int row = 16 * m + l16;
+            if constexpr (VEC)
+                s.load_rows(x, m, r, row < here ? row * K * 2 : kOOB, K, c0);
+            else
+                s.load_rows(x, m, some && row < here ? A + (int64_t)row * K : nullptr, K, c0);
+        }
     };
     auto load = [&](int block, int index, typename S::Words& b, bool some) {
         s.load_w4(b, 0, p.w, panel0 + index, (block * W + s.wave) * CW, some);
     };
     auto done = [&](int block, int index, int m, f32x4_t (&sum)[1]) {
-        f32x4_t* held = part + (index * MT + m) * 64 + lane;
-        if (block > 0)
-            sum[0] += *held;
-        if (block + 1 < p.blocks)
-            *held = sum[0];
-        else
-            store_tile(p, row0 + 16 * m, (int64_t)(panel0 + index) * 16, sum[0], fresh(lane));
+        if constexpr (!ONE) {
+            f32x4_t* held = part + (index * MT + m) * 64 + lane;
+            if (block > 0)
+                sum[0] += *held;
+            if (block + 1 < p.blocks) {
+                *held = sum[0];
+                return;
+            }
+        }
+        store_tile(p, row0 + 16 * m, (int64_t)(panel0 + index) * 16, sum[0], fresh(lane));
     };
-    s.run(p.blocks, n, rows, load, done);
+    if constexpr (ONE)
+        s.run_one(p.blocks, rows, load, done);
+    else
+        s.template run<4>(p.blocks, n, rows, load, done);
 }
+
+using One = std::integral_constant<int, 1>;
+using Two = std::integral_constant<int, 2>;
+using Four = std::integral_constant<int, 4>;
+
+// f(zero points?, MFMA steps between scales) as constants
+template <class F>
+static void by_storage(const W4View& w, const F& f)
+{
+    auto pick = [&](auto zero) {
+        w.group >= 128 ? f(zero, Four{}) : w.group == 64 ? f(zero, Two{}) : f(zero, One{});
+    };
+    w.zeros ? pick(std::true_type{}) : pick(std::false_type{});
+}
+
+static bool aligned_rows(const GemmW4Params& p) { return p.K % 8 == 0 && ((uintptr_t)p.A & 15u) == 0; }
 
 template <int MT, int W, int CW>
 static int launch_panels(GemmW4Params p, int per, hipStream_t s)
@@ -106,19 +127,24 @@ static int launch_panels(GemmW4Params p, int per, hipStream_t s)
     if (p.blocks > 1)
         per = (int)std::min<size_t>(per, (kLdsBytes - used) / (MT * 1024));
     p.per = per;
-    const size_t lds = p.blocks > 1 ? (size_t)per * MT * 1024 : 0;
+    // rows for two blocks at once do not fit in registers with MT = 4
+    const bool vec = aligned_rows(p), one = MT < 4 && vec && per == 1 && p.blocks > 1;
+    const size_t lds = p.blocks > 1 && !one ? (size_t)per * MT * 1024 : 0;
     const dim3 grid((unsigned)ceil_div(p.panels, per), (unsigned)ceil_div(p.M, 16 * MT)), block(64 * W);
-    if (p.w.zeros) {
-        if (p.w.group >= 128)
-            hipLaunchKernelGGL((gemm_w4_panels_kernel<true, MT, W, CW, 4>), grid, block, lds, s, p);
+    by_storage(p.w, [&](auto zero, auto gs) {
+        constexpr bool Z = decltype(zero)::value;
+        constexpr int G = decltype(gs)::value;
+        if constexpr (MT < 4) {
+            if (one) {
+                hipLaunchKernelGGL((gemm_w4_panels_kernel<Z, MT, W, CW, G, true, true>), grid, block, 0, s, p);
+                return;
+            }
+        }
+        if (vec)
+            hipLaunchKernelGGL((gemm_w4_panels_kernel<Z, MT, W, CW, G, true, false>), grid, block, lds, s, p);
         else
-            hipLaunchKernelGGL((gemm_w4_panels_kernel<true, MT, W, CW, 1>), grid, block, lds, s, p);
-    } else {
-        if (p.w.group >= 128)
-            hipLaunchKernelGGL((gemm_w4_panels_kernel<false, MT, W, CW, 4>), grid, block, lds, s, p);
-        else
-            hipLaunchKernelGGL((gemm_w4_panels_kernel<false, MT, W, CW, 1>), grid, block, lds, s, p);
-    }
+            hipLaunchKernelGGL((gemm_w4_panels_kernel<Z, MT, W, CW, G, false, false>), grid, block, lds, s, p);
+    });
     return launched("gemm_w4 launch");
 }
 
@@ -224,12 +250,12 @@ gemm_w4_tiled_kernel(GemmW4Params p)
             const int panel = panel0 + j;
             const bool some = panel < p.panels && c < chunks;
             const __amdgpu_buffer_rsrc_t rw =
-                make_rsrc(p.w.words + (int64_t)panel * chunks * 64, some ? (int64_t)chunks * 1024 : 0);
+                wave_rsrc(p.w.words + (int64_t)panel * chunks * 64, some ? (int64_t)chunks * 1024 : 0);
             const int64_t per = (int64_t)panel * p.w.groups * 16;
             const int n = some ? p.w.groups * 16 : 0;
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(
+            const __amdgpu_buffer_rsrc_t rs = wave_rsrc(
                 static_cast<const char*>(p.w.scales) + per * (p.w.scale_f32 ? 4 : 2), n * (p.w.scale_f32 ? 4 : 2));
-            const __amdgpu_buffer_rsrc_t rz = make_rsrc(p.w.zeros + (ZERO ? per : 0), n);
+            const __amdgpu_buffer_rsrc_t rz = wave_rsrc(p.w.zeros + (ZERO ? per : 0), n);
             b.w[j] = load16(rw, c * 1024 + lane * 16);
 #pragma unroll
             for (int q = 0; q < SC; ++q) {
@@ -330,9 +356,9 @@ gemm_w4_tiled_kernel(GemmW4Params p)
 template <int MT, int NT>
 static int launch_tiled(const GemmW4Params& p, hipStream_t s)
 {
-    const bool vec = p.K % 8 == 0 && ((uintptr_t)p.A & 15u) == 0;
+    const bool vec = aligned_rows(p);
     const dim3 grid((unsigned)(ceil_div(p.panels, 4 * NT) * ceil_div(p.M, 16 * MT))), block(256);
-    auto go = [&](auto zero, auto gs) {
+    by_storage(p.w, [&](auto zero, auto gs) {
         constexpr bool Z = decltype(zero)::value;
         constexpr int G = decltype(gs)::value;
         constexpr size_t lds = TiledW4<Z, MT, NT, G>::LDS;
@@ -340,14 +366,7 @@ static int launch_tiled(const GemmW4Params& p, hipStream_t s)
             hipLaunchKernelGGL((gemm_w4_tiled_kernel<Z, MT, NT, G, true>), grid, block, lds, s, p);
         else
             hipLaunchKernelGGL((gemm_w4_tiled_kernel<Z, MT, NT, G, false>), grid, block, lds, s, p);
-    };
-    using One = std::integral_constant<int, 1>;
-    using Two = std::integral_constant<int, 2>;
-    using Four = std::integral_constant<int, 4>;
-    auto pick = [&](auto zero) {
-        p.w.group >= 128 ? go(zero, Four{}) : p.w.group == 64 ? go(zero, Two{}) : go(zero, One{});
-    };
-    p.w.zeros ? pick(std::true_type{}) : pick(std::false_type{});
+    });
     return launched("gemm_w4 launch");
 }
 

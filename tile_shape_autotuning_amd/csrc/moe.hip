@@ -23,17 +23,10 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
-#include <type_traits>
 
-#include "panel_stream.hpp"
-#include "w4.hpp"
-#include "w4_host.hpp"
+#include "moe.hpp"
 
 namespace tg {
-
-static constexpr int kMaxExperts = 1024, kMaxChoices = 16;
-static constexpr int kTokens = 64;                     // tokens of one pass: a lane each
-static constexpr int kExpertWords = kMaxExperts / 32;
 
 // ---------------------------------------------------------------- routing
 struct RouteParams {
@@ -163,292 +156,6 @@ static int launch_route(const RouteParams& p, hipStream_t s)
 }
 
 // ---------------------------------------------------------------- experts
-// A stack of matrices [K -> N], one for each expert or two.
-struct ExpertStack {
-    const unsigned short* bf16;                        // [.., N, K]
-    W4View w4;                                         // matrix 0 of the stack
-    int64_t words, scales;                             // elements of w4.words / w4.scales from one matrix to the next
-    int N, K, panels;
-};
-
-__device__ __forceinline__ W4View matrix(const ExpertStack& s, int64_t i)
-{
-    W4View v = s.w4;
-    v.words += i * s.words;
-    v.scales = static_cast<const char*>(v.scales) + i * s.scales * (v.scale_f32 ? 4 : 2);
-    if (v.zeros)
-        v.zeros += i * s.scales;
-    return v;
-}
-
-struct MoeParams {
-    const unsigned short* x;                           // [T][H]
-    const int32_t* ids;                                // [T][k]
-    const float* weights;
-    unsigned* h;                                       // [T k][stride], two bf16: high half + low half
-    float* yp;                                         // [T k][H], each pair's part of y
-    unsigned short* y;                                 // [T][H]
-    ExpertStack up, down;
-    int64_t stride;                                    // I rounded up to 16
-    int T, E, k, H, I, gelu;
-    int up_per, up_blocks, down_per, down_blocks;      // panels a workgroup, blocks of the reduction
-};
-
-// The tokens that chose expert e, one a lane: lane r holds the r-th one's pair
-// index t k + j (its first choice of e) and the sum of its weights for e.
-// Returns how many.
-__device__ __forceinline__ int rows_of(const int* ids, const float* weights, int T, int k, int e, int lane, int& pair,
-                                       float& weight)
-{
-    int first = -1;
-    float w = 0.0f;
-    if (lane < T)
-        for (int j = k - 1; j >= 0; --j)
-            if (ids[lane * k + j] == e) {
-                first = lane * k + j;
-                if (weights)
-                    w += weights[first];
-            }
-    const unsigned long long has = __ballot(first >= 0);
-    const int rank = __popcll(has & ((1ull << lane) - 1));
-    // lanes without a row send theirs past the rows
-    const int to = 4 * (first >= 0 ? rank : __popcll(has) + (lane - rank));
-    pair = __builtin_amdgcn_ds_permute(to, first);
-    weight = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(w)));
-    return __popcll(has);
-}
-
-// Marks the chosen experts (all threads), copies ids to LDS; ends in a barrier.
-__device__ __forceinline__ void mark_experts(const int32_t* ids, int n, int E, int* copy, unsigned* bits)
-{
-    for (int i = threadIdx.x; i < kExpertWords; i += blockDim.x)
-        bits[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = ids[i];
-        copy[i] = e;
-        if (e >= 0 && e < E)
-            atomicOr(&bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-}
-
-// The chosen experts as a wave sees them: lane i < 32 holds bits of experts
-// 32 i .. 32 i + 31 and how many are chosen up to there.
-struct Chosen {
-    unsigned word;
-    int upto, count;
-    __device__ __forceinline__ Chosen(const unsigned* bits, int lane)
-    {
-        word = lane < kExpertWords ? bits[lane] : 0u;
-        upto = __popc(word);
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int o = __shfl_up(upto, off);
-            if (lane >= off)
-                upto += o;
-        }
-        count = __builtin_amdgcn_readlane(upto, 63);
-    }
-    // i-th chosen expert, i < count
-    __device__ __forceinline__ int expert(int i) const
-    {
-        const int at = __ffsll((long long)__ballot(upto > i)) - 1;
-        unsigned w = __builtin_amdgcn_readlane(word, at);
-        int skip = i - (__builtin_amdgcn_readlane(upto, at) - __popc(w));
-        for (; skip > 0; --skip)
-            w &= w - 1;
-        return at * 32 + __ffs((int)w) - 1;
-    }
-};
-
-__device__ __forceinline__ float gated(float g, float u, int gelu)
-{
-    return (gelu ? gelu_erf(g) : g / (1.0f + __expf(-g))) * u;
-}
-
-// The wave's share of a workgroup's work on one chosen expert: a stream of the
-// expert's panels past MT x 16 of its rows (panel_stream.hpp).
-struct Share {
-    int expert, rows, pair;                            // lane r: the r-th row's pair
-    float weight;
-};
-
-// False if there is no `slot`-th chosen expert.
-__device__ __forceinline__ bool share_of(const MoeParams& p, int slot, int* ids, unsigned* bits, const float* weights,
-                                         int lane, Share& s)
-{
-    mark_experts(p.ids, p.T * p.k, p.E, ids, bits);
-    const Chosen chosen(bits, lane);
-    if (slot >= chosen.count)
-        return false;
-    s.expert = chosen.expert(slot);
-    s.rows = rows_of(ids, weights, p.T, p.k, s.expert, lane, s.pair, s.weight);
-    return true;
-}
-
-template <bool W4F, bool ZERO, int MT, int W, int CW, int GS, bool VEC>
-__global__ void __launch_bounds__(64 * W) moe_up_kernel(MoeParams p)
-{
-    using S = PanelStream<W4F, ZERO, MT, 2, 1, W, CW, GS, 32>;
-    __shared__ f32x4_t red[S::RED], mid[S::MID];
-    __shared__ int ids[kTokens * kMaxChoices];
-    __shared__ unsigned bits[kExpertWords];
-    extern __shared__ f32x4_t part[];                  // [p.per][MT][2][64] if there is more than one block
-    S s(red, mid, p.up.w4.scale_f32);
-    const int lane = s.lane, l16 = lane & 15, kq = lane >> 4;
-    Share e;
-    if (!share_of(p, blockIdx.y, ids, bits, p.weights, lane, e))
-        return;
-    const int panel0 = blockIdx.x * p.up_per;
-    const int n = min(p.up_per, p.up.panels - panel0);
-    const int chunks = (p.H + 127) / 128;
-    W4View v[2];
-    const unsigned short* wb[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if constexpr (W4F)
-            v[j] = matrix(p.up, 2 * (int64_t)e.expert + j);
-        else
-            wb[j] = p.up.bf16 + (2 * (int64_t)e.expert + j) * p.I * p.H;
-    }
-
-    for (int r0 = 0; r0 < e.rows; r0 += 16 * MT) {
-        auto rows = [&](int block) {
-            const int c0 = (block * W + s.wave) * CW;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int r = r0 + 16 * m + l16;
-                const unsigned short* x = p.x + (int64_t)(__shfl(e.pair, r & 63) / p.k) * p.H;
-#pragma unroll
-                for (int i = 0; i < CW; ++i) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        s.a[i][m][0][t] = splat4(0);
-                    if (r < e.rows && c0 + i < chunks)
-                        load_chunk(s.a[i][m][0], x, c0 + i, kq, p.H);
-                }
-            }
-        };
-        auto load = [&](int block, int index, typename S::Words& b, bool some) {
-            const int c0 = (block * W + s.wave) * CW;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (W4F)
-                    s.load_w4(b, j, v[j], panel0 + index, c0, some);
-                else
-                    s.template load_bf16<VEC>(b, j, wb[j], p.I, p.H, panel0 + index, c0, some);
-            }
-        };
-        auto done = [&](int block, int index, int m, f32x4_t (&sum)[2]) {
-            f32x4_t* held = part + (index * MT + m) * 128 + lane;
-            if (block > 0) {
-                sum[0] += held[0];
-                sum[1] += held[64];
-            }
-            if (block + 1 < p.up_blocks) {
-                held[0] = sum[0];
-                held[64] = sum[1];
-                return;
-            }
-            const int at = fresh(lane), col = (panel0 + index) * 16 + (at & 15);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = r0 + 16 * m + (at >> 4) * 4 + r;
-                const int to = __shfl(e.pair, row & 63);
-                const float w = __shfl(e.weight, row & 63);
-                if (row >= e.rows)
-                    continue;
-                // columns past I stay zero for the second kernel
-                const float hv = col < p.I ? w * gated(sum[0][r], sum[1][r], p.gelu) : 0.0f;
-                const unsigned short hi = f32_to_bf16_rne(hv);
-                const float rest = hv - __uint_as_float((unsigned)hi << 16);
-                // an infinity or NaN stays one: its rest is no number
-                const unsigned short lo = (hi & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : (unsigned short)0;
-                p.h[(int64_t)to * p.stride + col] = (unsigned)hi << 16 | lo;
-            }
-        };
-        s.run(p.up_blocks, n, rows, load, done);
-    }
-}
-
-template <bool W4F, bool ZERO, int MT, int W, int CW, int GS, bool VEC>
-__global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p)
-{
-    using S = PanelStream<W4F, ZERO, MT, 1, 2, W, CW, GS, 32>;
-    __shared__ f32x4_t red[S::RED], mid[S::MID];
-    __shared__ int ids[kTokens * kMaxChoices];
-    __shared__ unsigned bits[kExpertWords];
-    extern __shared__ f32x4_t part[];                  // [p.per][MT][64] if there is more than one block
-    S s(red, mid, p.down.w4.scale_f32);
-    const int lane = s.lane, l16 = lane & 15, kq = lane >> 4;
-    Share e;
-    if (!share_of(p, blockIdx.y, ids, bits, nullptr, lane, e))
-        return;
-    const int panel0 = blockIdx.x * p.down_per;
-    const int n = min(p.down_per, p.down.panels - panel0);
-    W4View v;
-    const unsigned short* wb = nullptr;
-    if constexpr (W4F)
-        v = matrix(p.down, e.expert);
-    else
-        wb = p.down.bf16 + (int64_t)e.expert * p.H * p.I;
-
-    for (int r0 = 0; r0 < e.rows; r0 += 16 * MT) {
-        auto rows = [&](int block) {
-            const int c0 = (block * W + s.wave) * CW;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int r = r0 + 16 * m + l16;
-                const unsigned* h = p.h + (int64_t)__shfl(e.pair, r & 63) * p.stride;
-#pragma unroll
-                for (int i = 0; i < CW; ++i)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int64_t k = (int64_t)(c0 + i) * 128 + 32 * t + 8 * kq;
-                        u32x4_t h0 = splat4(0), h1 = splat4(0);
-                        if (r < e.rows && k < p.stride) {
-                            h0 = *reinterpret_cast<const u32x4_t*>(h + k);
-                            h1 = *reinterpret_cast<const u32x4_t*>(h + k + 4);
-                        }
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            const unsigned x0 = d < 2 ? h0[2 * d] : h1[2 * d - 4];
-                            const unsigned x1 = d < 2 ? h0[2 * d + 1] : h1[2 * d - 3];
-                            s.a[i][m][0][t][d] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
-                            s.a[i][m][1][t][d] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
-                        }
-                    }
-            }
-        };
-        auto load = [&](int block, int index, typename S::Words& b, bool some) {
-            const int c0 = (block * W + s.wave) * CW;
-            if constexpr (W4F)
-                s.load_w4(b, 0, v, panel0 + index, c0, some);
-            else
-                s.template load_bf16<VEC>(b, 0, wb, p.H, p.I, panel0 + index, c0, some);
-        };
-        auto done = [&](int block, int index, int m, f32x4_t (&sum)[1]) {
-            f32x4_t* held = part + (index * MT + m) * 64 + lane;
-            if (block > 0)
-                sum[0] += *held;
-            if (block + 1 < p.down_blocks) {
-                *held = sum[0];
-                return;
-            }
-            const int at = fresh(lane), col = (panel0 + index) * 16 + (at & 15);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = r0 + 16 * m + (at >> 4) * 4 + r;
-                const int from = __shfl(e.pair, row & 63);
-                if (row < e.rows && col < p.H)
-                    p.yp[(int64_t)from * p.H + col] = sum[0][r];
-            }
-        };
-        s.run(p.down_blocks, n, rows, load, done);
-    }
-}
-
 // y[t] = sum of the token's pairs, in the order of its choices.  Pairs that the
 // other kernels left out (no such expert, an expert's second mention) are
 // skipped here by the same rule.
@@ -469,92 +176,10 @@ __global__ void __launch_bounds__(256) moe_sum_kernel(MoeParams p)
     p.y[(int64_t)t * p.H + col] = f32_to_bf16_rne(v);
 }
 
-// Panels of a workgroup: two workgroups a compute unit over all chosen experts
-// (at most), as far as the sums of the reduction's earlier blocks find room in
-// LDS beside the `used` bytes.
-static int panels_per(int panels, int slots, int blocks, size_t used, size_t panel_bytes)
-{
-    int64_t per = std::max<int64_t>(1, (int64_t)panels * slots / (2 * kCus));
-    if (blocks > 1)
-        per = std::min<int64_t>(per, (int64_t)((kLdsBytes - used) / panel_bytes));
-    return (int)std::min<int64_t>(per, panels);
-}
-
-template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
-static void run_up(MoeParams p, hipStream_t s)
-{
-    constexpr int W = 8;
-    using S = PanelStream<W4F, ZERO, MT, 2, 1, W, CW, GS, 32>;
-    constexpr size_t used = (S::RED + S::MID) * 16 + (kTokens * kMaxChoices + kExpertWords) * 4;
-    static_assert(used + MT * 2048 <= kLdsBytes, "LDS");
-    const int slots = std::min(p.E, p.T * p.k);
-    p.up_blocks = (int)ceil_div(ceil_div(p.H, 128), W * CW);
-    p.up_per = panels_per(p.up.panels, slots, p.up_blocks, used, MT * 2048);
-    const size_t lds = p.up_blocks > 1 ? (size_t)p.up_per * MT * 2048 : 0;
-    const dim3 grid((unsigned)ceil_div(p.up.panels, p.up_per), (unsigned)slots);
-    hipLaunchKernelGGL((moe_up_kernel<W4F, ZERO, MT, W, CW, GS, VEC>), grid, dim3(64 * W), lds, s, p);
-}
-
-template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
-static void run_down(MoeParams p, hipStream_t s)
-{
-    constexpr int W = 8;
-    using S = PanelStream<W4F, ZERO, MT, 1, 2, W, CW, GS, 32>;
-    constexpr size_t used = (S::RED + S::MID) * 16 + (kTokens * kMaxChoices + kExpertWords) * 4;
-    static_assert(used + MT * 1024 <= kLdsBytes, "LDS");
-    const int slots = std::min(p.E, p.T * p.k);
-    p.down_blocks = (int)ceil_div(ceil_div(p.I, 128), W * CW);
-    p.down_per = panels_per(p.down.panels, slots, p.down_blocks, used, MT * 1024);
-    const size_t lds = p.down_blocks > 1 ? (size_t)p.down_per * MT * 1024 : 0;
-    const dim3 grid((unsigned)ceil_div(p.down.panels, p.down_per), (unsigned)slots);
-    hipLaunchKernelGGL((moe_down_kernel<W4F, ZERO, MT, W, CW, GS, VEC>), grid, dim3(64 * W), lds, s, p);
-}
-
-// Picks the instantiation for a weight: f.template go<W4F, ZERO, MT, CW, GS, VEC>(p, s).
-template <class F>
-static void dispatch(const tg_weight& w, int T, int64_t K, const MoeParams& p, hipStream_t s)
-{
-    const bool many = T > 16;
-    if (w.format == TG_W_W4) {
-        const bool two = K > 1024;                     // chunks a wave
-        auto pick = [&](auto zero, auto gs) {
-            constexpr bool Z = decltype(zero)::value;
-            constexpr int G = decltype(gs)::value;
-            if (many)
-                two ? F::template go<true, Z, 2, 2, G, true>(p, s) : F::template go<true, Z, 2, 1, G, true>(p, s);
-            else
-                two ? F::template go<true, Z, 1, 2, G, true>(p, s) : F::template go<true, Z, 1, 1, G, true>(p, s);
-        };
-        using One = std::integral_constant<int, 1>;
-        using Four = std::integral_constant<int, 4>;
-        if (w.zeros)
-            w.group >= 128 ? pick(std::true_type{}, Four{}) : pick(std::true_type{}, One{});
-        else
-            w.group >= 128 ? pick(std::false_type{}, Four{}) : pick(std::false_type{}, One{});
-    } else if (K % 8 == 0) {
-        many ? F::template go<false, false, 2, 1, 4, true>(p, s) : F::template go<false, false, 1, 1, 4, true>(p, s);
-    } else {
-        many ? F::template go<false, false, 2, 1, 4, false>(p, s) : F::template go<false, false, 1, 1, 4, false>(p, s);
-    }
-}
-
-struct Up {
-    template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
-    static void go(const MoeParams& p, hipStream_t s) { run_up<W4F, ZERO, MT, CW, GS, VEC>(p, s); }
-};
-struct Down {
-    template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
-    static void go(const MoeParams& p, hipStream_t s) { run_down<W4F, ZERO, MT, CW, GS, VEC>(p, s); }
-};
-
 static int launch_pass(const MoeParams& p, const tg_weight& up, const tg_weight& down, hipStream_t s)
 {
-    dispatch<Up>(up, p.T, p.H, p, s);
-    int st = launched("moe gate and up launch");
-    if (st != TG_OK)
-        return st;
-    dispatch<Down>(down, p.T, p.I, p, s);
-    if ((st = launched("moe down launch")) != TG_OK)
+    int st = launch_up(p, up, s);
+    if (st != TG_OK || (st = launch_down(p, down, s)) != TG_OK)
         return st;
     hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)ceil_div(p.H, 256), (unsigned)p.T), dim3(256), 0, s, p);
     return launched("moe sum launch");

@@ -33,11 +33,12 @@ __device__ __forceinline__ void lds_barrier()
 
 // MT: tiles of 16 rows; NT: matrices that share the rows (their panels advance
 // together); NA: A is the sum of NA bf16; W: waves; CW: chunks a wave; GS: MFMA
-// steps of 32 k between two scales (4: groups of 128 and more, 1: smaller).
+// steps of 32 k between two scales (4 for groups of 128 and more, else group / 32).
 // HALF: KiB of LDS for the sums of the panels between two barriers (held twice).
 template <bool W4F, bool ZERO, int MT, int NT, int NA, int W, int CW, int GS, int HALF>
 struct PanelStream {
     static constexpr int SC = W4F ? 4 / GS : 1;
+    static constexpr int GL = (CW * SC + 3) / 4;                               // loads of four scales each
     // panels between two barriers: as many as HALF KiB of LDS hold, four at most
     static constexpr int R0 = HALF / (W * MT * NT), R = R0 < 1 ? 1 : R0 > 4 ? 4 : R0;
     static constexpr int RED = 2 * R * W * MT * NT * 64;                       // f32x4 of LDS
@@ -45,11 +46,13 @@ struct PanelStream {
 
     struct Words {
         u32x4_t w[NT][CW][W4F ? 1 : 4];
-        unsigned s[NT][CW][SC];                        // the dword that holds the scale, as loaded
-        unsigned char z[NT][CW][ZERO ? SC : 1];        // zero point
+        unsigned s[NT][GL];                            // lane (i, column): the dword that holds scale i, as loaded
+        unsigned char z[NT][ZERO ? GL : 1];            // its zero point
+    };
+    struct Rows {
+        u32x4_t a[CW][MT][NA][4];
     };
 
-    u32x4_t a[CW][MT][NA][4];
     f32x4_t* red;
     f32x4_t* mid;                                      // this wave's part
     int lane, wave, turn;
@@ -66,26 +69,26 @@ struct PanelStream {
     // The wave's chunks c0 .. c0 + CW - 1 of panel `panel` of v, for matrix j of
     // the step.  What lies past the chunks, the groups or, with `some` false,
     // all of it, is out of the buffers' ranges: read as zero, without a fetch.
+    // One load brings four scales of the column, one to each quarter of the wave.
     __device__ __forceinline__ void load_w4(Words& b, int j, const W4View& v, int panel, int c0, bool some) const
     {
-        const int l16 = lane & 15;
         const __amdgpu_buffer_rsrc_t rw =
-            make_rsrc(v.words + (int64_t)panel * v.chunks * 64, some ? (int64_t)v.chunks * 1024 : 0);
+            wave_rsrc(v.words + (int64_t)panel * v.chunks * 64, some ? (int64_t)v.chunks * 1024 : 0);
         const int64_t per = (int64_t)panel * v.groups * 16;
         const int n = some ? v.groups * 16 : 0;
         const __amdgpu_buffer_rsrc_t rs =
-            make_rsrc(static_cast<const char*>(v.scales) + per * (v.scale_f32 ? 4 : 2), n * (v.scale_f32 ? 4 : 2));
-        const __amdgpu_buffer_rsrc_t rz = make_rsrc(v.zeros + (ZERO ? per : 0), n);
+            wave_rsrc(static_cast<const char*>(v.scales) + per * (v.scale_f32 ? 4 : 2), n * (v.scale_f32 ? 4 : 2));
+        const __amdgpu_buffer_rsrc_t rz = wave_rsrc(v.zeros + (ZERO ? per : 0), n);
 #pragma unroll
-        for (int i = 0; i < CW; ++i) {
+        for (int i = 0; i < CW; ++i)
             b.w[j][i][0] = load16_stream(rw, (c0 + i) * 1024 + lane * 16);
 #pragma unroll
-            for (int q = 0; q < SC; ++q) {
-                const int at = (int)((unsigned)((c0 + i) * 128 + 32 * GS * q) / (unsigned)v.group) * 16 + l16;
-                b.s[j][i][q] = load4(rs, v.scale_f32 ? at * 4 : at / 2 * 4);
-                if constexpr (ZERO)
-                    b.z[j][i][q] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
-            }
+        for (int l = 0; l < GL; ++l) {
+            const int i = CW * SC == 1 ? 0 : 4 * l + (lane >> 4);
+            const int at = (int)((unsigned)(c0 * 128 + 32 * GS * i) / (unsigned)v.group) * 16 + (lane & 15);
+            b.s[j][l] = load4(rs, v.scale_f32 ? at * 4 : at / 2 * 4);
+            if constexpr (ZERO)
+                b.z[j][l] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
         }
     }
 
@@ -99,13 +102,13 @@ struct PanelStream {
         const int l16 = lane & 15, rows = min(16, N - panel * 16);
         const unsigned short* base = m + (int64_t)panel * 16 * K;
         if constexpr (VEC) {
-            const __amdgpu_buffer_rsrc_t r = make_rsrc(base, some ? (int64_t)rows * K * 2 : 0);
+            const __amdgpu_buffer_rsrc_t r = wave_rsrc(base, some ? (int64_t)rows * K * 2 : 0);
 #pragma unroll
             for (int i = 0; i < CW; ++i)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const int k = (c0 + i) * 128 + 32 * t + 8 * (lane >> 4);
-                    b.w[j][i][t] = load16_stream(r, k < K ? (l16 * K + k) * 2 : kOOB);
+                    b.w[j][i][t] = load16(r, k < K ? (l16 * K + k) * 2 : kOOB);
                 }
         } else {
 #pragma unroll
@@ -120,9 +123,65 @@ struct PanelStream {
         }
     }
 
-    // After the fragments are set: their constant sums.
-    __device__ __forceinline__ void correct()
+    // The wave's fragments of row tile m: `off` bytes to the lane's row of K bf16
+    // in r, kOOB if it has none.
+    __device__ __forceinline__ void load_rows(Rows& x, int m, __amdgpu_buffer_rsrc_t r, int off, int K, int c0) const
     {
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int k = (c0 + i) * 128 + 32 * t + 8 * (lane >> 4);
+                x.a[i][m][0][t] = load16(r, off != kOOB && k < K ? off + k * 2 : kOOB);
+            }
+    }
+    // Of a row that starts anywhere, with any K (NULL: none).
+    __device__ __forceinline__ void load_rows(Rows& x, int m, const unsigned short* row, int K, int c0) const
+    {
+#pragma unroll
+        for (int i = 0; i < CW; ++i) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                x.a[i][m][0][t] = splat4(0);
+            if (row && c0 + i < (K + 127) / 128)
+                load_chunk(x.a[i][m][0], row, c0 + i, lane >> 4, K);
+        }
+    }
+    // Of a row of pairs of bf16, high half the larger (NA = 2): as stored, for settle to part.
+    __device__ __forceinline__ void load_pairs(Rows& x, int m, __amdgpu_buffer_rsrc_t r, int off, int K, int c0) const
+    {
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int k = (c0 + i) * 128 + 32 * t + 8 * (lane >> 4);
+                const int at = off != kOOB && k < K ? off + k * 4 : kOOB;
+                x.a[i][m][0][t] = load16(r, at);
+                x.a[i][m][NA - 1][t] = load16(r, at == kOOB ? kOOB : at + 16);
+            }
+    }
+
+    // Makes loaded rows ready: parts the pairs, computes the constant sums.
+    __device__ __forceinline__ void settle(Rows& x)
+    {
+        if constexpr (NA == 2) {
+#pragma unroll
+            for (int i = 0; i < CW; ++i)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const u32x4_t p = x.a[i][m][0][t], q = x.a[i][m][1][t];
+                        x.a[i][m][0][t] = u32x4_t{__builtin_amdgcn_perm(p[1], p[0], 0x07060302u),
+                                                  __builtin_amdgcn_perm(p[3], p[2], 0x07060302u),
+                                                  __builtin_amdgcn_perm(q[1], q[0], 0x07060302u),
+                                                  __builtin_amdgcn_perm(q[3], q[2], 0x07060302u)};
+                        x.a[i][m][1][t] = u32x4_t{__builtin_amdgcn_perm(p[1], p[0], 0x05040100u),
+                                                  __builtin_amdgcn_perm(p[3], p[2], 0x05040100u),
+                                                  __builtin_amdgcn_perm(q[1], q[0], 0x05040100u),
+                                                  __builtin_amdgcn_perm(q[3], q[2], 0x05040100u)};
+                    }
+        }
         if constexpr (W4F) {
             const f32x4_t none = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -136,9 +195,9 @@ struct PanelStream {
                         for (int t = q * GS; t < (q + 1) * GS; ++t)
 #pragma unroll
                             for (int n = 0; n < NA; ++n) {
-                                c = mfma_bf16(a[i][m][n][t], splat4(kCentre), c);
+                                c = mfma_bf16(x.a[i][m][n][t], splat4(kCentre), c);
                                 if constexpr (ZERO)
-                                    s = mfma_bf16(a[i][m][n][t], splat4(kOnes), s);
+                                    s = mfma_bf16(x.a[i][m][n][t], splat4(kOnes), s);
                             }
                         // the same in every column: lanes 0, 16, 32, 48 have all rows
                         const int at = ((i * SC + q) * MT + m) * 4 + (lane >> 4);
@@ -155,24 +214,34 @@ struct PanelStream {
         }
     }
 
-    __device__ __forceinline__ void multiply(f32x4_t (&total)[MT][NT], const Words& b) const
+    __device__ __forceinline__ void multiply(f32x4_t (&total)[MT][NT], const Rows& x, const Words& b) const
     {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
+        if constexpr (W4F) {
+            // scales and shifts, still with the quarter that loaded them
+            float scale[NT][GL], shift[NT][GL];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                total[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < CW; ++i) {
-            if constexpr (W4F) {
+                for (int l = 0; l < GL; ++l) {
+                    scale[j][l] = __uint_as_float((b.s[j][l] << up) & keep);
+                    shift[j][l] = ZERO ? 8.0f - (float)b.z[j][ZERO ? l : 0] : 0.0f;
+                }
+            auto from = [&](float v, int i) {
+                if constexpr (CW * SC == 1)
+                    return v;
+                return __int_as_float(
+                    __builtin_amdgcn_ds_bpermute(4 * (16 * (i & 3) + (lane & 15)), __float_as_int(v)));
+            };
+#pragma unroll
+            for (int i = 0; i < CW; ++i) {
                 f32x4_t acc[MT][NT];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const int q = t / GS;
+                    const int q = i * SC + t / GS;
                     if (t % GS == 0) {
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            const f32x4_t c = mid[((i * SC + q) * MT + m) * 4 + (lane >> 4)];
+                            const f32x4_t c = mid[(q * MT + m) * 4 + (lane >> 4)];
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
                                 acc[m][j] = c;
@@ -185,29 +254,33 @@ struct PanelStream {
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
                             for (int n = 0; n < NA; ++n)
-                                acc[m][j] = mfma_bf16(a[i][m][n][t], w, acc[m][j]);
+                                acc[m][j] = mfma_bf16(x.a[i][m][n][t], w, acc[m][j]);
                     }
                     if (t % GS == GS - 1) {
+                        float sc[NT], d[NT];
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            sc[j] = from(scale[j][q / 4], q);
+                            d[j] = ZERO ? from(shift[j][q / 4], q) : 0.0f;
+                        }
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             f32x4_t s = {0.f, 0.f, 0.f, 0.f};
                             if constexpr (ZERO)
-                                s = mid[CW * SC * MT * 4 + ((i * SC + q) * MT + m) * 4 + (lane >> 4)];
+                                s = mid[CW * SC * MT * 4 + (q * MT + m) * 4 + (lane >> 4)];
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                const float scale = __uint_as_float((b.s[j][i][q] << up) & keep);
-                                float d = 0.0f;
-                                if constexpr (ZERO)
-                                    d = 8.0f - (float)b.z[j][i][q];
+                            for (int j = 0; j < NT; ++j)
 #pragma unroll
                                 for (int r = 0; r < 4; ++r)
                                     total[m][j][r] =
-                                        fmaf(scale, ZERO ? fmaf(d, s[r], acc[m][j][r]) : acc[m][j][r], total[m][j][r]);
-                            }
+                                        fmaf(sc[j], ZERO ? fmaf(d[j], s[r], acc[m][j][r]) : acc[m][j][r], total[m][j][r]);
                         }
                     }
                 }
-            } else {
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CW; ++i)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -216,19 +289,25 @@ struct PanelStream {
                         for (int n = 0; n < NA; ++n)
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
-                                total[m][j] = mfma_bf16(a[i][m][n][t], b.w[j][i][t], total[m][j]);
-            }
+                                total[m][j] = mfma_bf16(x.a[i][m][n][t], b.w[j][i][t], total[m][j]);
         }
     }
 
-    // One panel: the wave's sums to LDS.  After every R panels, and the last,
-    // a barrier; then the waves share out the tiles and pass the sums over all
-    // waves to done(index, m, sums).
-    template <class Done>
-    __device__ __forceinline__ void step(int index, int n, const Words& b, const Done& done)
+    __device__ __forceinline__ void clear(f32x4_t (&total)[MT][NT]) const
     {
-        f32x4_t total[MT][NT];
-        multiply(total, b);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                total[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // The wave's sums of panel `index` to LDS.  After every R panels, and the
+    // last, a barrier; then the waves share out the tiles and pass the sums over
+    // all waves to done(index, m, sums).
+    template <class Done>
+    __device__ __forceinline__ void meet(int index, int n, const f32x4_t (&total)[MT][NT], const Done& done)
+    {
         f32x4_t* half = red + (turn & 1) * (RED / 2);
         f32x4_t* r = half + index % R * (W * MT * NT * 64);
 #pragma unroll
@@ -257,38 +336,83 @@ struct PanelStream {
 
     // Panels 0 .. n - 1 of the workgroup, in each of `blocks` blocks of the
     // reduction (both the same for all its waves): load(block, index, words,
-    // some) fills the wave's chunks, or skips them if !some; rows(block) sets
-    // its fragments; done(block, index, m, sums) as in step.  The next step's
-    // words are on their way across the change of blocks too.  No other branch
-    // goes round a load, and nothing is computed from a loaded value before
-    // its step: where two paths meet, or where a value is first used, the wait
-    // for it would come before the younger loads are out.  (Scales shifted
-    // into place as they were loaded: 42 us instead of 30 for 16 x 28672 x
-    // 8192.)
-    template <class Rows, class Load, class Done>
-    __device__ __forceinline__ void run(int blocks, int n, const Rows& rows, const Load& load, const Done& done)
+    // some) fills the wave's chunks and rows(block, rows, some) its fragments,
+    // or skip them if !some; done(block, index, m, sums) as in meet.  The words
+    // of the next D - 1 steps are on their way, across the change of blocks
+    // too.  No other branch goes round a load, and nothing is computed from a
+    // loaded value before its step: where two paths meet, or where a value is
+    // first used, the wait for it would come before the younger loads are out.
+    // (Scales shifted into place as they were loaded: 42 us instead of 30 for
+    // 16 x 28672 x 8192.)
+    template <int D, class RowsOf, class Load, class Done>
+    __device__ __forceinline__ void run(int blocks, int n, const RowsOf& rows, const Load& load, const Done& done)
+    {
+        static_assert(D >= 2 && D <= 4, "steps");
+        Words b[D];
+        Rows x;
+        int block = 0, index = 0, ahead_block = 0, ahead = 0;
+        auto fetch = [&](Words& to) {
+            load(ahead_block, ahead, to, ahead_block < blocks);
+            if (++ahead == n) {
+                ahead = 0;
+                ++ahead_block;
+            }
+        };
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d)
+            fetch(b[d]);
+        rows(0, x, true);
+        settle(x);
+        auto one = [&](int d) {
+            fetch(b[(d + D - 1) % D]);
+            f32x4_t total[MT][NT];
+            clear(total);
+            multiply(total, x, b[d]);
+            meet(index, n, total, [&](int i, int m, f32x4_t (&sum)[NT]) { done(block, i, m, sum); });
+            if (++index < n)
+                return true;
+            index = 0;
+            if (++block == blocks)
+                return false;
+            rows(block, x, true);
+            settle(x);
+            return true;
+        };
+        if constexpr (D == 2)
+            while (one(0) && one(1)) {
+            }
+        else if constexpr (D == 3)
+            while (one(0) && one(1) && one(2)) {
+            }
+        else
+            while (one(0) && one(1) && one(2) && one(3)) {
+            }
+    }
+
+    // The same for a single panel and many blocks: the next block's rows are on
+    // their way with its words, and the sums meet once, at the end.
+    template <class RowsOf, class Load, class Done>
+    __device__ __forceinline__ void run_one(int blocks, const RowsOf& rows, const Load& load, const Done& done)
     {
         Words b[2];
-        int block = 0, index = 0;
+        Rows x[2];
+        f32x4_t total[MT][NT];
+        clear(total);
+        int block = 0;
         load(0, 0, b[0], true);
-        rows(0);
-        correct();
-        auto one = [&](const Words& now, Words& next) {
-            const bool turns = index + 1 == n;
-            const int nb = turns ? block + 1 : block, ni = turns ? 0 : index + 1;
-            const bool more = nb < blocks;
-            load(more ? nb : block, ni, next, more);
-            step(index, n, now, [&](int i, int m, f32x4_t (&sum)[NT]) { done(block, i, m, sum); });
-            if (more && turns) {
-                rows(nb);
-                correct();
-            }
-            block = nb;
-            index = ni;
+        rows(0, x[0], true);
+        auto one = [&](const Words& now, Words& next, Rows& mine, Rows& after) {
+            const bool more = block + 1 < blocks;
+            load(block + 1, 0, next, more);
+            rows(block + 1, after, more);
+            settle(mine);
+            multiply(total, mine, now);
+            ++block;
             return more;
         };
-        while (one(b[0], b[1]) && one(b[1], b[0])) {
+        while (one(b[0], b[1], x[0], x[1]) && one(b[1], b[0], x[1], x[0])) {
         }
+        meet(0, 1, total, [&](int, int m, f32x4_t (&sum)[NT]) { done(0, 0, m, sum); });
     }
 };
 
