@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(64 * W) gemm_w4_panels_kernel(GemmW4Params p)
     const int K = (int)p.K, here = (int)min((int64_t)(16 * MT), p.M - row0);
     const unsigned short* A = p.A + row0 * K;
 
+    const W4Source source(p.w, panel0, p.panels);
     auto rows = [&](int block, typename S::Rows& x, bool some) {
         const int c0 = (block * W + s.wave) * CW;
         const __amdgpu_buffer_rsrc_t r = wave_rsrc(A, some ? (int64_t)here * K * 2 : 0);
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(64 * W) gemm_w4_panels_kernel(GemmW4Params p)
         }
     };
     auto load = [&](int block, int index, typename S::Words& b, bool some) {
-        s.load_w4(b, 0, p.w, panel0 + index, (block * W + s.wave) * CW, some);
+        s.load_w4(b, 0, source, index, (block * W + s.wave) * CW, some);
     };
     auto done = [&](int block, int index, int m, f32x4_t (&sum)[1]) {
         if constexpr (!ONE) {
@@ -126,6 +127,7 @@ static int launch_panels(GemmW4Params p, int per, hipStream_t s)
     static_assert(used + MT * 1024 <= kLdsBytes, "LDS");
     if (p.blocks > 1)
         per = (int)std::min<size_t>(per, (kLdsBytes - used) / (MT * 1024));
+    per = std::min(per, panels_in_reach(p.w.chunks));
     p.per = per;
     // rows for two blocks at once do not fit in registers with MT = 4
     const bool vec = aligned_rows(p), one = MT < 4 && vec && per == 1 && p.blocks > 1;

@@ -153,7 +153,7 @@ inline int panels_per(int panels, const MoeParams& p, int resident, int blocks, 
     int64_t per = ceil_div(panels, std::min(each, panels));
     if (blocks > 1)
         per = std::min<int64_t>(per, (int64_t)((kLdsBytes - used) / panel_bytes));
-    return (int)per;
+    return (int)std::min<int64_t>(per, panels_in_reach((std::max(p.H, p.I) + 127) / 128));
 }
 
 // Workgroups of a kernel that a compute unit holds.

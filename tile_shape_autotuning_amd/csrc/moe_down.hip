@@ -20,12 +20,8 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p)
         return;
     const int panel0 = blockIdx.x * p.down_per;
     const int n = min(p.down_per, p.down.panels - panel0);
-    W4View v;
-    const unsigned short* wb = nullptr;
-    if constexpr (W4F)
-        v = matrix(p.down, e.expert);
-    else
-        wb = p.down.bf16 + (int64_t)e.expert * p.H * p.I;
+    const W4Source v(matrix(p.down, e.expert), panel0, p.down.panels);
+    const unsigned short* wb = p.down.bf16 + (W4F ? 0 : (int64_t)e.expert * p.H * p.I);
 
     for (int r0 = 0; r0 < e.rows; r0 += 16 * MT) {
         auto rows = [&](int block, typename S::Rows& x, bool some) {
@@ -40,7 +36,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p)
         auto load = [&](int block, int index, typename S::Words& b, bool some) {
             const int c0 = (block * W + s.wave) * CW;
             if constexpr (W4F)
-                s.load_w4(b, 0, v, panel0 + index, c0, some);
+                s.load_w4(b, 0, v, index, c0, some);
             else
                 s.template load_bf16<VEC>(b, 0, wb, p.H, p.I, panel0 + index, c0, some);
         };

@@ -27,15 +27,9 @@ __global__ void __launch_bounds__(64 * W) moe_up_kernel(MoeParams p)
         return;
     const int panel0 = blockIdx.x * p.up_per;
     const int n = min(p.up_per, p.up.panels - panel0);
-    W4View v[2];
-    const unsigned short* wb[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if constexpr (W4F)
-            v[j] = matrix(p.up, 2 * (int64_t)e.expert + j);
-        else
-            wb[j] = p.up.bf16 + (2 * (int64_t)e.expert + j) * p.I * p.H;
-    }
+    const W4Source v[2] = {W4Source(matrix(p.up, 2 * (int64_t)e.expert), panel0, p.up.panels),
+                           W4Source(matrix(p.up, 2 * (int64_t)e.expert + 1), panel0, p.up.panels)};
+    const unsigned short* wb = p.up.bf16 + (W4F ? 0 : 2 * (int64_t)e.expert * p.I * p.H);
 
     for (int r0 = 0; r0 < e.rows; r0 += 16 * MT) {
         auto rows = [&](int block, typename S::Rows& x, bool some) {
@@ -55,9 +49,9 @@ __global__ void __launch_bounds__(64 * W) moe_up_kernel(MoeParams p)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if constexpr (W4F)
-                    s.load_w4(b, j, v[j], panel0 + index, c0, some);
+                    s.load_w4(b, j, v[j], index, c0, some);
                 else
-                    s.template load_bf16<VEC>(b, j, wb[j], p.I, p.H, panel0 + index, c0, some);
+                    s.template load_bf16<VEC>(b, j, wb + (int64_t)j * p.I * p.H, p.I, p.H, panel0 + index, c0, some);
             }
         };
         auto done = [&](int block, int index, int m, f32x4_t (&sum)[2]) {

@@ -31,6 +31,32 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// A matrix of 4-bit weights of `panels` panels from panel `first` on; the byte
+// counts are what buffer loads are checked against.
+struct W4Source {
+    const void *words, *scales, *zeros;
+    int word_bytes, scale_bytes, zero_bytes;
+    float per_chunk;                                   // groups a chunk
+    int chunks, groups, scale_f32;
+
+    __device__ __forceinline__ W4Source(const W4View& v, int first, int panels)
+        : words(v.words + (int64_t)first * v.chunks * 64),
+          scales(static_cast<const char*>(v.scales) + (int64_t)first * v.groups * (v.scale_f32 ? 64 : 32)),
+          zeros(v.zeros ? v.zeros + (int64_t)first * v.groups * 16 : nullptr),
+          word_bytes(bytes((int64_t)(panels - first) * v.chunks * 1024)),
+          scale_bytes(bytes((int64_t)(panels - first) * v.groups * (v.scale_f32 ? 64 : 32))),
+          zero_bytes(v.zeros ? bytes((int64_t)(panels - first) * v.groups * 16) : 0),
+          per_chunk(128.0f / (float)v.group), chunks(v.chunks), groups(v.groups), scale_f32(v.scale_f32)
+    {
+    }
+
+private:
+    static __device__ __forceinline__ int bytes(int64_t n)
+    {
+        return (int)(n < kMaxRecords ? n : kMaxRecords);
+    }
+};
+
 // MT: tiles of 16 rows; NT: matrices that share the rows (their panels advance
 // together); NA: A is the sum of NA bf16; W: waves; CW: chunks a wave; GS: MFMA
 // steps of 32 k between two scales (4 for groups of 128 and more, else group / 32).
@@ -66,29 +92,31 @@ struct PanelStream {
         mid = m + (W4F ? wave * (MID / W) : 0);
     }
 
-    // The wave's chunks c0 .. c0 + CW - 1 of panel `panel` of v, for matrix j of
-    // the step.  What lies past the chunks, the groups or, with `some` false,
-    // all of it, is out of the buffers' ranges: read as zero, without a fetch.
-    // One load brings four scales of the column, one to each quarter of the wave.
-    __device__ __forceinline__ void load_w4(Words& b, int j, const W4View& v, int panel, int c0, bool some) const
+    // The wave's chunks c0 .. c0 + CW - 1 of the source's panel `index`, for
+    // matrix j of the step.  What lies past the chunks, the groups or, with
+    // `some` false, all of it, gets an offset out of the buffers' ranges: read
+    // as zero, without a fetch.  One load brings four scales of the column, one
+    // to each quarter of the wave.
+    __device__ __forceinline__ void load_w4(Words& b, int j, const W4Source& v, int index, int c0, bool some) const
     {
-        const __amdgpu_buffer_rsrc_t rw =
-            wave_rsrc(v.words + (int64_t)panel * v.chunks * 64, some ? (int64_t)v.chunks * 1024 : 0);
-        const int64_t per = (int64_t)panel * v.groups * 16;
-        const int n = some ? v.groups * 16 : 0;
-        const __amdgpu_buffer_rsrc_t rs =
-            wave_rsrc(static_cast<const char*>(v.scales) + per * (v.scale_f32 ? 4 : 2), n * (v.scale_f32 ? 4 : 2));
-        const __amdgpu_buffer_rsrc_t rz = wave_rsrc(v.zeros + (ZERO ? per : 0), n);
+        const __amdgpu_buffer_rsrc_t rw = wave_rsrc(v.words, v.word_bytes);
+        const __amdgpu_buffer_rsrc_t rs = wave_rsrc(v.scales, v.scale_bytes);
+        const __amdgpu_buffer_rsrc_t rz = wave_rsrc(v.zeros, v.zero_bytes);
 #pragma unroll
-        for (int i = 0; i < CW; ++i)
-            b.w[j][i][0] = load16_stream(rw, (c0 + i) * 1024 + lane * 16);
+        for (int i = 0; i < CW; ++i) {
+            const int at = some && c0 + i < v.chunks ? (index * v.chunks + c0 + i) * 1024 : kOOB;
+            b.w[j][i][0] = load16_stream(rw, (int)((unsigned)at + (unsigned)(lane * 16)));
+        }
 #pragma unroll
         for (int l = 0; l < GL; ++l) {
             const int i = CW * SC == 1 ? 0 : 4 * l + (lane >> 4);
-            const int at = (int)((unsigned)(c0 * 128 + 32 * GS * i) / (unsigned)v.group) * 16 + (lane & 15);
-            b.s[j][l] = load4(rs, v.scale_f32 ? at * 4 : at / 2 * 4);
+            // groups of whole chunks by a product: off by 2^-23 of a number that is half a chunk from any border
+            const int g = GS == 4 ? (int)(((float)(c0 + i) + 0.5f) * v.per_chunk) : c0 * SC + i;
+            const bool in = some && g < v.groups;
+            const int at = (index * v.groups + g) * 16 + (lane & 15);
+            b.s[j][l] = load4(rs, in ? (v.scale_f32 ? at * 4 : at / 2 * 4) : kOOB);
             if constexpr (ZERO)
-                b.z[j][l] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
+                b.z[j][l] = __builtin_amdgcn_raw_buffer_load_b8(rz, in ? at : kOOB, 0, 0);
         }
     }
 

@@ -66,16 +66,22 @@ struct W4View {
     int chunks, groups;                        // ceil(K / 128), ceil(K / group)
 };
 
-// make_rsrc of values that are the same in the whole wave, said so: where the
-// compiler's analysis loses track of that it would wrap every load in a loop
-// over the lanes' descriptors.
+// A pointer that is the same in the whole wave, said so: where the compiler's
+// analysis loses track of that it wraps every buffer load in a loop over the
+// lanes' descriptors.
+__device__ __forceinline__ const void* same_in_wave(const void* p)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return reinterpret_cast<const void*>(
+        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) << 32 |
+        (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a));
+}
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rsrc(const void* base, int64_t bytes)
 {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) << 32 |
-                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
     const int64_t n = bytes < 0 ? 0 : (bytes > kMaxRecords ? kMaxRecords : bytes);
-    return make_rsrc(reinterpret_cast<const void*>(u), __builtin_amdgcn_readfirstlane((int)n));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(same_in_wave(base)), (short)0,
+                                             __builtin_amdgcn_readfirstlane((int)n), kRsrcWord3);
 }
 
 // Sixteen bytes from any element address: one load, the hardware takes it unaligned.

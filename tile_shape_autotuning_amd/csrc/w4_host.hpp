@@ -32,6 +32,9 @@ inline W4View view_w4(const tg_weight& w, int64_t K, int64_t N, int64_t i)
     return v;
 }
 
+// Panels of `chunks` KiB that a workgroup's 32-bit offsets reach.
+inline int panels_in_reach(int chunks) { return (1 << 20) / chunks; }
+
 inline int launched(const char* what)
 {
     const hipError_t e = hipGetLastError();
