@@ -46,20 +46,41 @@ __device__ __forceinline__ unsigned order_key(float v)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float logit_of(unsigned key)
+{
+    return key & 0x80000000u ? __uint_as_float(key & 0x7FFFFFFFu) : __uint_as_float(~key);
+}
+
+// Lane 63 combines all lanes through the data-parallel primitives (six
+// instructions; shuffles through LDS took the routing of 16384 x 256 from XX to
+// 17 us): shifts within rows of 16, then each row's last lane to the next.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned moved(unsigned v)
+{
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+
 __device__ __forceinline__ unsigned wave_max(unsigned v)
 {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v = max(v, (unsigned)__shfl_xor((int)v, off));
-    return v;
+    v = max(v, moved<0x111, 0xf>(v));
+    v = max(v, moved<0x112, 0xf>(v));
+    v = max(v, moved<0x114, 0xf>(v));
+    v = max(v, moved<0x118, 0xf>(v));
+    v = max(v, moved<0x142, 0xa>(v));
+    v = max(v, moved<0x143, 0xc>(v));
+    return (unsigned)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 __device__ __forceinline__ float wave_sum(float v)
 {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off);
-    return v;
+    auto add = [&](unsigned o) { v += __uint_as_float(o); };
+    add(moved<0x111, 0xf>(__float_as_uint(v)));
+    add(moved<0x112, 0xf>(__float_as_uint(v)));
+    add(moved<0x114, 0xf>(__float_as_uint(v)));
+    add(moved<0x118, 0xf>(__float_as_uint(v)));
+    add(moved<0x142, 0xa>(__float_as_uint(v)));
+    add(moved<0x143, 0xc>(__float_as_uint(v)));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 // One wave routes one token; lane l holds experts l, l + 64, ...  The k largest
@@ -85,14 +106,14 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, int
         best = max(best, key[i]);
     }
     best = wave_max(best);
-    const float top = best & 0x80000000u ? __uint_as_float(best & 0x7FFFFFFFu) : __uint_as_float(~best);
+    const float top = logit_of(best);
     float all = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
         all += lane + 64 * i < p.E ? expf(v[i] - top) : 0.0f;
     all = wave_sum(all);
     const bool empty = top == -INFINITY;
-    float mine = 0.0f, chosen = 0.0f;                  // lane j keeps the j-th choice
+    unsigned mine = 0;                                 // lane j keeps the j-th choice
     int mine_id = 0;
     for (int j = 0; j < p.k; ++j) {
         unsigned m = 0;
@@ -107,25 +128,20 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, int
             if (hit)
                 id = 64 * i + __ffsll((long long)hit) - 1;
         }
-        float l = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (id == lane + 64 * i) {
-                l = v[i];
-                key[i] = 0;
-            }
-        }
-        l = __shfl(l, id & 63);
-        const float e = empty ? 0.0f : expf(l - top);
-        chosen += e;
+        for (int i = 0; i < V; ++i)
+            key[i] = id == lane + 64 * i ? 0u : key[i];
         if (lane == j) {
-            mine = e;
+            mine = m;
             mine_id = id;
         }
     }
+    // the key gives the logit back (a zero's sign apart)
+    const float e = lane < p.k && !empty ? expf(logit_of(mine) - top) : 0.0f;
+    const float sum = p.renorm ? wave_sum(e) : all;
     if (lane < p.k) {
         ids[lane] = mine_id;
-        weights[lane] = empty ? 0.0f : mine / (p.renorm ? chosen : all);
+        weights[lane] = empty ? 0.0f : e / sum;
     }
 }
 
