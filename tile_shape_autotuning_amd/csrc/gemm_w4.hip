@@ -421,7 +421,7 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
     if (M <= 32)
         return launch_panels<2, 16, 1>(p, per, s);
     if (M <= 64)
-        return launch_panels<4, 8, 2>(p, per, s);
+        return p.w.chunks <= 8 ? launch_panels<4, 8, 1>(p, per, s) : launch_panels<4, 8, 2>(p, per, s);
     // 64 x 256 tiles where two workgroups a compute unit have one, 64 x 128 where
     // one has, else 64 x 64: 2048 x 4096 x 4096 77, 85 and 112 us, 100 x 28672 x
     // 4096 59, 50 and 66, 128 x 4096 x 4096 58, 38 and 30.  (128 x 256 leaves

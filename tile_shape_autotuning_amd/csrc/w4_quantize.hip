@@ -15,7 +15,9 @@
 // share a column, so a group's extremes are those of a lane's own elements and
 // two shuffles.  A matrix stored [N][K] has a lane's eight rows contiguous and
 // is read straight into registers, and its values written back the same way; one
-// stored [K][N] crosses LDS, which turns rows of 64 columns into columns.
+// stored [K][N] crosses LDS, which turns rows of 64 columns into columns.  The
+// latter's accesses are of whole lines and carry the non-temporal policy; the
+// former's are of parts of lines, which the caches join.
 // Groups of more than 128 rows are read twice, first for the extremes.
 #include <hip/hip_runtime.h>
 
@@ -134,9 +136,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(QuantParams p)
                     u32x4_t x[X];
 #pragma unroll
                     for (int q = 0; q < X; ++q)
-                        x[q] = col < p.N && k + q * 4 < p.K
-                                   ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from) + q)
-                                   : splat4(0);
+                        x[q] = col < p.N && k + q * 4 < p.K ? reinterpret_cast<const u32x4_t*>(from)[q] : splat4(0);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         if constexpr (BF16)
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(QuantParams p)
 #pragma unroll
                     for (int q = 0; q < X; ++q)
                         if (col < p.N && k + q * 4 < p.K)
-                            __builtin_nontemporal_store(x[q], reinterpret_cast<u32x4_t*>(to) + q);
+                            reinterpret_cast<u32x4_t*>(to)[q] = x[q];
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
