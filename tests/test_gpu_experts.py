@@ -101,7 +101,12 @@ GEMMS = [(1, 16, 128, 128, False, "bf16"), (1, 1, 1, 32, True, "f32"), (3, 17, 3
          (16, 4096, 1024, 128, False, "bf16"), (17, 100, 1000, 64, True, "f32"), (33, 48, 777, 32, True, "f32"),
          (64, 1001, 776, 256, False, "bf16"), (65, 80, 128, 32, False, "f32"), (130, 257, 640, 128, True, "bf16"),
          (1, 40, 9000, 1024, True, "bf16"), (300, 272, 520, 64, False, "bf16"), (5, 16, 2100, 384, True, "f32"),
-         (129, 513, 1031, 128, False, "f32"), (257, 520, 2048, 32, True, "bf16"), (2, 3000, 96, 64, False, "bf16")]
+         (129, 513, 1031, 128, False, "f32"), (257, 520, 2048, 32, True, "bf16"), (2, 3000, 96, 64, False, "bf16"),
+         # several panels a workgroup and several blocks of K, one and two and four row tiles, rows of any alignment
+         (3, 5000, 4400, 128, True, "bf16"), (20, 100, 2304, 64, False, "f32"), (20, 5000, 2305, 256, True, "f32"),
+         (50, 4200, 2400, 32, False, "bf16"), (33, 64, 1024, 128, True, "bf16"), (9, 4112, 6150, 64, False, "f32"),
+         # K below one fragment, and not a whole fragment past whole ones
+         (70, 33, 5, 32, False, "f32"), (70, 33, 135, 32, True, "bf16"), (18, 20, 1, 128, False, "bf16")]
 
 
 @pytest.mark.parametrize("M,N,K,group,zero,scale", GEMMS)
@@ -237,7 +242,11 @@ def _check_mlp(y, x, ids, w, gate, up, down, act, kind):
 MLPS = [(1, 4, 2, 64, 32, "bf16", "silu"), (1, 1, 1, 8, 1, "bf16", "gelu"), (3, 5, 2, 100, 37, "bf16", "silu"),
         (16, 8, 4, 128, 200, "w4", "silu"), (17, 3, 2, 96, 130, "w4", "gelu"), (40, 2, 1, 264, 72, "bf16", "gelu"),
         (64, 40, 6, 136, 64, "w4", "silu"), (65, 4, 3, 33, 50, "w4", "silu"), (130, 6, 2, 72, 136, "bf16", "silu"),
-        (64, 1, 1, 48, 40, "bf16", "silu"), (5, 1024, 16, 16, 16, "bf16", "silu"), (2, 3, 2, 1200, 300, "w4", "silu")]
+        (64, 1, 1, 48, 40, "bf16", "silu"), (5, 1024, 16, 16, 16, "bf16", "silu"), (2, 3, 2, 1200, 300, "w4", "silu"),
+        # several blocks of the reduction, with one panel a workgroup and with more, with one and two row tiles
+        (1, 2, 2, 4104, 1000, "bf16", "silu"), (2, 2, 2, 4104, 1000, "w4", "gelu"), (1, 3, 1, 500, 4104, "bf16", "silu"),
+        (3, 2, 1, 520, 4104, "w4", "silu"), (2, 1, 1, 2304, 9000, "w4", "silu"), (20, 2, 1, 2056, 1100, "bf16", "silu"),
+        (24, 2, 2, 2100, 1300, "w4", "silu"), (2, 3, 1, 1101, 1277, "bf16", "gelu"), (33, 2, 1, 301, 77, "bf16", "silu")]
 
 
 def _choices(rng, T, E, k):
@@ -356,6 +365,62 @@ def test_a_block_on_two_streams_and_in_two_graphs():
         torch.cuda.synchronize()
         for (_, r), w in zip(graphs, want):
             assert all(torch.equal(a, b) for a, b in zip(r, w)), f"replay {turn}"
+
+
+def test_a_first_call_may_be_captured():
+    rng = np.random.default_rng(31)
+    up, down, g, u, d = _experts(rng, 3, 40, 56, "w4", 32, False, "f32")
+    x = rng.integers(-2, 3, (26, 40)).astype(np.float64)
+    ids, w = _choices(rng, 26, 3, 2)
+    xd, idd, wd = _bf16(x), _cuda(ids), _cuda(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = tg.moe_mlp(xd, idd, wd, up, down)
+    for _ in range(3):
+        y.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_mlp(y, x, ids, w.astype(np.float64), g, u, d, "silu", "w4")
+
+
+def test_every_entry_point_takes_nothing():
+    q, _ = _w4(np.random.default_rng(0), (), 64, 32, 32, True, "f32")
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    assert tg.gemm_w4(torch.empty((0, 64), **bf), q).shape == (0, 32)
+    ids, w = tg.moe_route(torch.empty((0, 5), device="cuda"), 2)
+    assert ids.shape == (0, 2) and w.shape == (0, 2)
+    up, down = torch.zeros((5, 2, 8, 16), **bf), torch.zeros((5, 16, 8), **bf)
+    assert tg.moe_mlp(torch.empty((0, 16), **bf), ids, w, up, down).shape == (0, 16)
+    assert tg.moe_layer(torch.empty((0, 16), **bf), torch.empty((0, 5), device="cuda"), up, down, 2)[0].shape == (0, 16)
+    none, values = tg.w4_quantize(torch.empty((0, 64, 32), device="cuda"), 32, zero_point=True, values=True)
+    assert none.words.shape == (0, 2, 1, 64, 4) and values.shape == (0, 64, 32)
+
+
+def test_refusals_on_the_gpu_leave_the_output():
+    q, _ = _w4(np.random.default_rng(0), (), 64, 32, 32, False, "bf16")
+    A = torch.ones((4, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((4, 32), 9.0, device="cuda")
+    for bad in (A[:, ::2], A.float(), A[:, :32].contiguous()):
+        with pytest.raises((ValueError, TypeError)):
+            tg.gemm_w4(bad, q, out=out)
+    for b in (q._replace(group=48), q._replace(N=48), q._replace(scales=q.scales[..., :8]), q._replace(words=q.words.long()),
+              q._replace(zeros=torch.zeros(3, dtype=torch.uint8, device="cuda")), q._replace(words=q.words.cpu())):
+        with pytest.raises(ValueError):
+            tg.gemm_w4(A, b, out=out)
+    with pytest.raises(ValueError):
+        tg.gemm_w4(A, q, torch.zeros(31, device="cuda"))
+    with pytest.raises(tg.TileGemmError):
+        tg.moe_route(torch.zeros((2, 1025), device="cuda"), 2)
+    with pytest.raises(ValueError):
+        tg.w4_quantize(torch.zeros((64, 32), device="cuda")[::2])
+    ids, w = torch.zeros((4, 1), dtype=torch.int32, device="cuda"), torch.ones((4, 1), device="cuda")
+    up = torch.zeros((2, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        tg.moe_mlp(A, ids, w, up, torch.zeros((3, 64, 8), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        tg.moe_layer(A, torch.zeros((4, 3), device="cuda"), up, up, 1)
+    assert bool((out == 9.0).all())
 
 
 def test_quantised_weights_serve_the_product():
