@@ -455,9 +455,10 @@ typedef enum {
  * round is to fp32, then to scale_dtype; rint of the exact quotient, ties to
  * even.  A group whose scale is zero has codes that stand for zero; one that
  * holds an infinity or NaN, or whose range overflows fp32, has values that
- * are NaN.  Storage past K and N is written as zero.  Asynchronous on the
- * stream of tg_set_stream, as are all functions of this section; none of
- * them allocates, so each may be captured into a graph.
+ * are NaN.  Storage past K and N is written as zero.  The outputs must not
+ * overlap W.  Asynchronous on the stream of tg_set_stream, as are all
+ * functions of this section; none of them allocates, so each may be captured
+ * into a graph.  Bad arguments are TG_E_INVAL, before anything is queued.
  * Limits: K, N <= 2^21, count <= 65535 (TG_E_UNSUPPORTED).
  */
 int tg_w4_quantize(int64_t count, int64_t K, int64_t N, int group, const void *W, int dtype, int rows_first,
@@ -495,7 +496,7 @@ int tg_moe_route(int64_t T, int64_t E, int k, const void *logits, int dtype, int
  * elsewhere); an expert that a token names twice counts with both weights; a
  * token without experts gets zeros.  workspace: device memory of
  * tg_moe_workspace_bytes(T, H, I, k), 16-byte aligned, not shared by calls that
- * may overlap.  Tokens are taken 64 at a time: every 64 read the experts that
+ * may overlap.  y must not overlap the inputs.  Tokens are taken 64 at a time: every 64 read the experts that
  * they chose once.  The same call gives the same bits.
  * Limits: H, I <= 65536 and those of tg_moe_route (TG_E_UNSUPPORTED).
  */

@@ -105,6 +105,9 @@ GEMMS = [(1, 16, 128, 128, False, "bf16"), (1, 1, 1, 32, True, "f32"), (3, 17, 3
          # several panels a workgroup and several blocks of K, one and two and four row tiles, rows of any alignment
          (3, 5000, 4400, 128, True, "bf16"), (20, 100, 2304, 64, False, "f32"), (20, 5000, 2305, 256, True, "f32"),
          (50, 4200, 2400, 32, False, "bf16"), (33, 64, 1024, 128, True, "bf16"), (9, 4112, 6150, 64, False, "f32"),
+         # each tile size of the kernel for many rows, groups within a chunk with and without zero points
+         (1030, 8200, 264, 64, True, "bf16"), (1030, 8200, 200, 128, False, "f32"), (1025, 8192, 130, 32, True, "f32"),
+         (300, 6700, 136, 32, True, "f32"), (300, 6700, 392, 256, True, "bf16"), (150, 600, 700, 64, True, "f32"),
          # K below one fragment, and not a whole fragment past whole ones
          (70, 33, 5, 32, False, "f32"), (70, 33, 135, 32, True, "bf16"), (18, 20, 1, 128, False, "bf16")]
 

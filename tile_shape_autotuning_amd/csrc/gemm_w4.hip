@@ -159,8 +159,9 @@ static int launch_panels(GemmW4Params p, int per, hipStream_t s)
 // (w4.hpp) are computed one chunk ahead, each wave a quarter of the rows, and
 // start the accumulators.  One barrier a chunk; it and the transfers are
 // covered by the other workgroups of the compute unit (two of 256 registers
-// with NT = 4, three with NT = 2).  Bound by issue: 2048 x 4096 x 4096 77 us, 0.9
-// PFLOP/s; 4096 x 8192 x 8192 525 us, 1.05 PFLOP/s.
+// with NT = 4, three with NT = 2).  Bound by issue: 2048 x 4096 x 4096 75 us, 0.9
+// PFLOP/s (zero points 93; groups of 64 86 and 141, of 32 103 and 141); 4096 x
+// 8192 x 8192 501 us, 1.1 PFLOP/s.
 //
 // Stage layout: row r of A, 256 bytes, 16-byte piece q at q ^ swz<16>(r): the
 // 16 rows of a fragment read hit 16 different pieces.
@@ -241,10 +242,12 @@ gemm_w4_tiled_kernel(GemmW4Params p)
             }
         }
     };
+    // With several groups a chunk, each quarter of the wave holds one's scale and
+    // zero point.
     struct Words {
         u32x4_t w[NT];
-        unsigned s[NT][SC];
-        unsigned char z[NT][ZERO ? SC : 1];
+        unsigned s[NT];
+        unsigned char z[NT];
     };
     auto load = [&](int c, Words& b) {
 #pragma unroll
@@ -259,13 +262,11 @@ gemm_w4_tiled_kernel(GemmW4Params p)
                 static_cast<const char*>(p.w.scales) + per * (p.w.scale_f32 ? 4 : 2), n * (p.w.scale_f32 ? 4 : 2));
             const __amdgpu_buffer_rsrc_t rz = wave_rsrc(p.w.zeros + (ZERO ? per : 0), n);
             b.w[j] = load16(rw, c * 1024 + lane * 16);
-#pragma unroll
-            for (int q = 0; q < SC; ++q) {
-                const int at = (int)((unsigned)(c * 128 + 32 * GS * q) / (unsigned)p.w.group) * 16 + l16;
-                b.s[j][q] = load4(rs, p.w.scale_f32 ? at * 4 : at / 2 * 4);
-                if constexpr (ZERO)
-                    b.z[j][q] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
-            }
+            const int k = c * 128 + (SC == 1 ? 0 : 32 * GS * min(kq, SC - 1));
+            const int at = (int)((unsigned)k / (unsigned)p.w.group) * 16 + l16;
+            b.s[j] = load4(rs, p.w.scale_f32 ? at * 4 : at / 2 * 4);
+            if constexpr (ZERO)
+                b.z[j] = __builtin_amdgcn_raw_buffer_load_b8(rz, at, 0, 0);
         }
     };
 
@@ -278,6 +279,10 @@ gemm_w4_tiled_kernel(GemmW4Params p)
 
     auto multiply = [&](int c, const Words& b) {
         const f32x4_t* from = mids + (c & 1) * T::MIDS;
+        float scale[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            scale[j] = __uint_as_float((b.s[j] << up) & keep);
         f32x4_t acc[MT][NT];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -300,25 +305,39 @@ gemm_w4_tiled_kernel(GemmW4Params p)
                     acc[m][j] = mfma_bf16(a, w[j], acc[m][j]);
             }
             if (t % GS == GS - 1) {
-                float scale[NT], d[NT];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    scale[j] = __uint_as_float((b.s[j][q] << up) & keep);
-                    if constexpr (ZERO)
-                        d[j] = 8.0f - (float)b.z[j][q];
-                }
+                    const float sc = SC == 1 ? scale[j]
+                                             : __int_as_float(__builtin_amdgcn_ds_bpermute(
+                                                   4 * (16 * q + l16), __float_as_int(scale[j])));
+                    float d = 0.0f;
+                    if constexpr (ZERO && SC == 1)
+                        d = 8.0f - (float)b.z[j];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    f32x4_t s;
-                    if constexpr (ZERO)
-                        s = from[(SC * MT + q * MT + m) * 4 + kq];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int m = 0; m < MT; ++m) {
+                        f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+                        if constexpr (ZERO && SC == 1)
+                            s = from[(MT + m) * 4 + kq];
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            total[m][j][r] =
-                                fmaf(scale[j], ZERO ? fmaf(d[j], s[r], acc[m][j][r]) : acc[m][j][r], total[m][j][r]);
+                            total[m][j][r] = fmaf(
+                                sc, ZERO && SC == 1 ? fmaf(d, s[r], acc[m][j][r]) : acc[m][j][r], total[m][j][r]);
+                    }
                 }
+                // the scheduler would begin all groups at once, and spill
+                if constexpr (SC > 1)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // (8 - z) sum A of several groups: one fp32 MFMA a tile, whose k is the group
+        if constexpr (ZERO && SC > 1) {
+            const float* sums = reinterpret_cast<const float*>(from + SC * MT * 4);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float sum = kq < SC ? sums[(kq * MT + m) * 16 + l16] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    total[m][j] = mfma_f32(sum, kq < SC ? scale[j] * (8.0f - (float)b.z[j]) : 0.0f, total[m][j]);
             }
         }
     };
@@ -362,7 +381,9 @@ static int launch_tiled(const GemmW4Params& p, hipStream_t s)
     const dim3 grid((unsigned)(ceil_div(p.panels, 4 * NT) * ceil_div(p.M, 16 * MT))), block(256);
     by_storage(p.w, [&](auto zero, auto gs) {
         constexpr bool Z = decltype(zero)::value;
-        constexpr int G = decltype(gs)::value;
+        // groups of 64 with zero points as pairs of 32: the kernel for two groups a chunk spills (2048 x 4096 x
+        // 4096 565 us, so 141)
+        constexpr int G = Z && decltype(gs)::value == 2 ? 1 : decltype(gs)::value;
         constexpr size_t lds = TiledW4<Z, MT, NT, G>::LDS;
         if (vec)
             hipLaunchKernelGGL((gemm_w4_tiled_kernel<Z, MT, NT, G, true>), grid, block, lds, s, p);

@@ -1,6 +1,6 @@
 // What the kernels of the expert layer share (moe.hip has the overview): the
-// call's parameters, and how a workgroup finds its expert and that expert's
-// tokens.
+// call's parameters, how a workgroup finds its expert and that expert's tokens,
+// and how the work is divided.
 #pragma once
 
 #include <algorithm>
@@ -135,7 +135,8 @@ __device__ __forceinline__ bool share_of(const MoeParams& p, int slot, int* ids,
     return true;
 }
 
-// Steps whose words are held or on their way: 4-bit words are small.
+// Steps whose words are held or on their way: 4-bit words are small (gate and up
+// of 64 experts of 2048 x 1408: 49 us with four, 52 with two).
 template <bool W4F>
 constexpr int kDepth = W4F ? 4 : 2;
 
@@ -161,9 +162,11 @@ template <class Kernel>
 inline int resident_on_cu(Kernel kernel, int threads)
 {
     int n = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != hipSuccess || n < 1)
-        n = 1;
-    return n;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != hipSuccess) {
+        (void)hipGetLastError();
+        return 1;
+    }
+    return std::max(n, 1);
 }
 
 // F::go<W4F, ZERO, MT, CW, GS, VEC>(p, s) for a weight whose reduction has K

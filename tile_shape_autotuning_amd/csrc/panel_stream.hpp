@@ -7,11 +7,16 @@
 // reduction is therefore cut among the W waves of a workgroup: a wave keeps
 // its rows' fragments of CW chunks (128 k each) in registers, for all panels
 // that the workgroup works on, and a step is the CW chunks of the next panel,
-// whose loads are all issued one step ahead.  In flight are CW KiB a wave in 4
-// bits, four times that in bf16, and A is read once a workgroup rather than
-// once a panel.  The waves' sums of a panel meet in LDS, in wave order, after one
-// barrier that leaves the loads in flight; the buffer is doubled, and the wave
-// that adds a tile up takes turns, so nobody waits for the adding.
+// whose loads are all issued one to three steps ahead.  A is read once a
+// workgroup rather than once a panel.  The waves' sums meet in LDS and are added
+// in wave order.  One barrier, which leaves the loads in flight, serves up to
+// four panels: their tiles are then added up by as many waves at once, while
+// the others go on in the other half of the buffer.  For 16 rows of 28672 x
+// 8192 in 4 bits: loads of a panel for every wave's own A 79 us, rows kept and
+// panels streamed 42, scales left as loaded until their step 30, a barrier for
+// four panels and the next block's words ahead 27 (31 with zero points, 4.0
+// TB/s; what is left over the 24 us of a copy is the start of the stream, the
+// meeting of the sums and 36 VALU instructions a KiB of codes).
 //
 // The constant parts of the 4-bit sums (the two brackets of w4.hpp that do not
 // depend on the column) are computed once for each chunk when the fragments
