@@ -292,6 +292,20 @@ def test_moe_mlp_storage_forms(group, zero, scale):
     _check_mlp(y, x, ids, w.astype(np.float64), g, u, d, "silu", "w4")
 
 
+@pytest.mark.parametrize("T", [2, 30])
+def test_moe_mlp_takes_each_projection_in_its_own_form(T):
+    rng = np.random.default_rng(T)
+    E, k, H, I = 4, 3, 72, 88
+    x = rng.integers(-2, 3, (T, H)).astype(np.float64)
+    ids, w = _choices(rng, T, E, k)
+    up4, down4, g4, u4, d4 = _experts(rng, E, H, I, "w4", 64, False, "f32")
+    up16, down16, g16, u16, d16 = _experts(rng, E, H, I, "bf16")
+    for up, down, g, u, d, kind in ((up4, down16, g4, u4, d16, "bf16"), (up16, down4, g16, u16, d4, "w4")):
+        y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down)
+        torch.cuda.synchronize()
+        _check_mlp(y, x, ids, w.astype(np.float64), g, u, d, "silu", kind)
+
+
 @pytest.mark.parametrize("T,E,k,kind", [(1, 8, 2, "w4"), (4, 70, 8, "bf16"), (17, 33, 4, "w4"), (70, 9, 2, "bf16")])
 def test_moe_layer_is_route_then_mlp(T, E, k, kind):
     rng = np.random.default_rng(T)

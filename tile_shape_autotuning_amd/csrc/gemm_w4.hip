@@ -410,7 +410,7 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
         return set_error(TG_E_UNSUPPORTED, "K and N are at most 2^21, M at most 2^20");
     if (M == 0 || N == 0)
         return TG_OK;
-    const int st = check_weight(B, K, N, "gemm_w4");
+    const int st = check_weight(B, "gemm_w4");
     if (st != TG_OK)
         return st;
     if (B->format != TG_W_W4)
@@ -421,7 +421,7 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
         return set_error(TG_E_UNSUPPORTED, "no HIP device");
     GemmW4Params p{};
     p.A = static_cast<const unsigned short*>(A);
-    p.w = view_w4(*B, K, N, 0);
+    p.w = view_w4(*B, K);
     p.bias = bias;
     p.C = C;
     p.M = M;

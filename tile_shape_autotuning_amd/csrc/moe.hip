@@ -210,11 +210,9 @@ static int launch_pass(const MoeParams& p, const tg_weight& up, const tg_weight&
 static ExpertStack stack_of(const tg_weight& w, int64_t K, int64_t N)
 {
     ExpertStack s{};
-    s.N = (int)N;
-    s.K = (int)K;
     s.panels = (int)ceil_div(N, 16);
     if (w.format == TG_W_W4) {
-        s.w4 = view_w4(w, K, N, 0);
+        s.w4 = view_w4(w, K);
         s.words = (int64_t)s.panels * s.w4.chunks * 64;
         s.scales = (int64_t)s.panels * s.w4.groups * 16;
     } else {
@@ -263,7 +261,7 @@ static int check_mlp(int64_t T, int64_t H, int64_t I, int64_t E, int k, const vo
         return set_error(TG_E_INVAL, "unknown gate activation");
     if (T == 0)
         return TG_OK;
-    if ((st = check_weight(up, H, I, "gate_up")) != TG_OK || (st = check_weight(down, I, H, "down")) != TG_OK)
+    if ((st = check_weight(up, "gate_up")) != TG_OK || (st = check_weight(down, "down")) != TG_OK)
         return st;
     if (!x || !y || (((uintptr_t)x | (uintptr_t)y) & 1u))
         return set_error(TG_E_INVAL, "x and y must be given, aligned to their elements");

@@ -21,7 +21,7 @@ struct ExpertStack {
     const unsigned short* bf16;                        // [.., N, K]
     W4View w4;                                         // matrix 0 of the stack
     int64_t words, scales;                             // elements of w4.words / w4.scales from one matrix to the next
-    int N, K, panels;
+    int panels;
 };
 
 __device__ __forceinline__ W4View matrix(const ExpertStack& s, int64_t i)

@@ -13,22 +13,20 @@ constexpr int kCus = 256;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// TG_OK, or the error (set) for a K x N weight of `w`'s format.
-int check_weight(const tg_weight* w, int64_t K, int64_t N, const char* name);
+// TG_OK, or the error (set) that a call reports for weight `name`.
+int check_weight(const tg_weight* w, const char* name);
 
-// The i-th K x N matrix of a stack of 4-bit weights.
-inline W4View view_w4(const tg_weight& w, int64_t K, int64_t N, int64_t i)
+// The first matrix, with K rows, of a stack of 4-bit weights.
+inline W4View view_w4(const tg_weight& w, int64_t K)
 {
     W4View v{};
-    const int64_t panels = ceil_div(N, 16);
     v.group = w.group;
     v.scale_f32 = w.scale_dtype == TG_F32;
     v.chunks = (int)ceil_div(K, 128);
     v.groups = (int)ceil_div(K, w.group);
-    v.words = static_cast<const u32x4_t*>(w.data) + i * panels * v.chunks * 64;
-    const int64_t at = i * panels * v.groups * 16;
-    v.scales = static_cast<const char*>(w.scales) + at * (v.scale_f32 ? 4 : 2);
-    v.zeros = w.zeros ? static_cast<const unsigned char*>(w.zeros) + at : nullptr;
+    v.words = static_cast<const u32x4_t*>(w.data);
+    v.scales = w.scales;
+    v.zeros = static_cast<const unsigned char*>(w.zeros);
     return v;
 }
 

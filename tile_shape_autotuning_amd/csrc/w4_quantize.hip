@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(QuantParams p)
     }
 }
 
-int check_weight(const tg_weight* w, int64_t K, int64_t N, const char* name)
+int check_weight(const tg_weight* w, const char* name)
 {
     const std::string s(name);
     if (!w || !w->data)
@@ -343,8 +343,6 @@ int check_weight(const tg_weight* w, int64_t K, int64_t N, const char* name)
         return set_error(TG_E_INVAL, s + ": scales are fp32 or bf16");
     if (w->group != 32 && w->group != 64 && (w->group < 128 || w->group % 128 != 0))
         return set_error(TG_E_INVAL, s + ": group must be 32, 64 or a multiple of 128");
-    (void)K;
-    (void)N;
     return TG_OK;
 }
 
@@ -367,7 +365,7 @@ extern "C" int tg_w4_quantize(int64_t count, int64_t K, int64_t N, int group, co
     w.scales = scales;
     if (count == 0)
         w.data = w.scales = reinterpret_cast<void*>(16);   // nothing is read or written
-    const int st = check_weight(&w, K, N, "w4_quantize");
+    const int st = check_weight(&w, "w4_quantize");
     if (st != TG_OK)
         return st;
     const int64_t span = group > kQRows ? group : kQRows;
