@@ -1,0 +1,137 @@
+"""4-bit weights and expert layers where they can go wrong: the hidden state's
+precision, hot experts, rows near overflow, gates far from zero, groups that
+are not finite.  The fp64 oracle and the helpers are those of test_gpu_experts.
+"""
+import numpy as np
+import pytest
+
+from oracle import experts_ref as R
+
+from gpu_util import mark
+from test_gpu_experts import _bf16, _choices, _cuda, _experts, _gpu, _np, _w4, tg, torch    # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- the hidden state
+def _lone_neurons(rng, T, E, I):
+    """Integer experts of which one hidden neuron in 128 is not zero: x [T, 2], gate and up [E, 2, I, 2] and the
+    neurons.  Gates are near 700 (gate(g) = g in fp32, SiLU and GELU), hidden values 700^2 - s^2, s <= 12: integers
+    of 19 bits whose differences bf16 holds."""
+    x = np.stack([np.full(T, 175.0), rng.integers(1, 4, T)], 1)
+    up = np.zeros((E, 2, I, 2))
+    at = np.array([c + int(rng.integers(min(128, I - c))) for c in range(0, I, 128)])
+    up[:, 0, :, 0] = 4.0
+    up[:, 0, :, 1] = rng.integers(-4, 5, (E, I))
+    up[:, 1, at, 0] = 4.0
+    up[:, 1, at, 1] = -up[:, 0, at, 1]
+    return x, up, at
+
+
+def _pair_columns(rng, E, I, H, at):
+    """[E, I, H]: each column takes one of the neurons with 1, 2 or 3 and another with the opposite."""
+    d = np.zeros((E, I, H))
+    for e in range(E):
+        for n in range(H):
+            i, j = rng.choice(at, 2, replace=False)
+            a = rng.integers(1, 4)
+            d[e, i, n], d[e, j, n] = a, -a
+    return d
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("kind,group,zero", [("bf16", 0, False), ("w4", 128, False), ("w4", 64, True), ("w4", 32, True)])
+@pytest.mark.parametrize("T,E,I", [(3, 2, 520), (2, 2, 2600), (40, 2, 520), (40, 2, 1300), (40, 2, 2600), (3, 2, 301)])
+def test_hidden_values_keep_24_bits(T, E, I, kind, group, zero, act):
+    # h <= 700^2 < 2^24 / 31, alone in its chunk: every sum, the 4-bit product's constant parts (31 h, 24 h)
+    # included, is an integer below 2^24 and exact in fp32, so y is the difference of two h, rounded once to bf16
+    rng = np.random.default_rng(I + T + group)
+    H = 48
+    x, up, at = _lone_neurons(rng, T, E, I)
+    d = _pair_columns(rng, E, I, H, at)
+    x = np.concatenate([x, np.zeros((T, H - 2))], 1)
+    up = np.concatenate([up, np.zeros((E, 2, I, H - 2))], 3)
+    ids = np.tile(np.arange(E, dtype=np.int32), (T, 1))
+    ids[:, 1] = -1                                     # one expert a token: its sums stand alone
+    ids[::2, 0] = 1
+    if T > 16:
+        assert T * ids.shape[1] > 8 * E                # two row tiles
+    w = np.ones(ids.shape, np.float32)
+    if kind == "bf16":
+        down = _bf16(d.transpose(0, 2, 1))
+    else:
+        P, G = -(-H // 16), -(-I // group)
+        z = rng.integers(4, 12, (E, P, G, 16), dtype=np.uint8) if zero else None
+        words = []
+        for e in range(E):
+            zk = np.full((I, H), 8) if z is None else \
+                z[e].transpose(1, 0, 2).reshape(G, P * 16)[:, :H].repeat(group, 0)[:I].astype(int)
+            words.append(R.pack(d[e].astype(int) + zk))
+        down = tg.W4(_cuda(np.stack(words)), torch.ones((E, P, G, 16), device="cuda"), _cuda(z) if zero else None,
+                     I, H, group)
+    mark(f"hidden values T{T} E{E} I{I} {kind} g{group} {act}")
+    y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), _bf16(up), down, gate=act)
+    torch.cuda.synchronize()
+    h = np.einsum("th,eih->tei", x, up[:, 0]) * np.einsum("th,eih->tei", x, up[:, 1])
+    ref = np.stack([h[t, ids[t, 0]] @ d[ids[t, 0]] for t in range(T)])
+    assert np.abs(h).max() * 31 < 2 ** 24
+    assert np.array_equal(_np(y), R.round_bf16(ref))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "w4"])
+def test_infinite_hidden_values_stay_infinite(kind):
+    # bf16 experts: an infinite hidden value meets the formula's infinities, and NaN only where it meets a zero weight
+    x = torch.ones((3, 16), device="cuda", dtype=torch.bfloat16)
+    x[1] = 3e38                                        # gate 3e38 * 16 overflows
+    up = torch.ones((1, 2, 8, 16), device="cuda", dtype=torch.bfloat16)
+    up[0, 1, 1:] = 0.0                                 # neuron 0 alone is infinite; 0 * inf gives NaN elsewhere
+    up[0, 0, 1:] = 0.0
+    down = torch.zeros((1, 16, 8), device="cuda", dtype=torch.bfloat16)
+    down[0, :, 0] = torch.tensor([1.0, -2.0] * 8, device="cuda")
+    if kind == "w4":
+        with_codes = tg.w4_quantize(down.transpose(1, 2), 32)
+        y = tg.moe_mlp(x, torch.zeros((3, 1), dtype=torch.int32, device="cuda"), torch.ones((3, 1), device="cuda"), up,
+                       with_codes)
+        assert bool(torch.isnan(y[1]).all()) and bool(torch.isfinite(y[[0, 2]]).all())
+        return
+    y = tg.moe_mlp(x, torch.zeros((3, 1), dtype=torch.int32, device="cuda"), torch.ones((3, 1), device="cuda"), up, down)
+    inf = float("inf")
+    assert y[1].tolist() == [inf, -inf] * 8 and bool(torch.isfinite(y[[0, 2]]).all())
+
+
+@pytest.mark.parametrize("T,E,k,H,I,kind,group,zero", [(64, 8, 2, 512, 640, "bf16", 0, False),
+                                                       (64, 8, 2, 512, 640, "w4", 64, True),
+                                                       (48, 32, 4, 512, 2304, "w4", 128, False)])
+def test_outputs_round_once(T, E, k, H, I, kind, group, zero):
+    # How many bf16 outputs may differ from the rounded exact ones: a sum off by d is rounded otherwise with
+    # probability d / step.  d in units of the root of the sum of the squares of its terms: at most 48 fp32
+    # additions one after the other (three parts of 4 fragments, two chunks a wave, eight waves, k pairs), off by
+    # 2^-24 on average where sums are truncated, of partial sums up to the root (4 bits: the constant parts'
+    # 24 against 7.5 of a code's own on average, 3.2 times, and a chunk at a time): 3e-6, 9e-6.  A hidden state in
+    # one bf16 would be off by 1e-3.
+    rng = np.random.default_rng(T + H + group)
+    x = R.round_bf16(rng.standard_normal((T, H)))
+    if kind == "bf16":
+        u = R.round_bf16(rng.standard_normal((E, 2, I, H)) / np.sqrt(H))
+        d = R.round_bf16(rng.standard_normal((E, H, I)) / np.sqrt(I))
+        up, down = _bf16(u), _bf16(d)
+        g, u, d = u[:, 0].transpose(0, 2, 1), u[:, 1].transpose(0, 2, 1), d.transpose(0, 2, 1)
+    else:
+        up, u = _w4(rng, (E, 2), H, I, group, zero, "f32", powers=(0.3 / np.sqrt(H), 0.2 / np.sqrt(H)))
+        down, d = _w4(rng, (E,), I, H, group, zero, "f32", powers=(0.3 / np.sqrt(I), 0.2 / np.sqrt(I)))
+        g, u = u[:, 0], u[:, 1]
+    ids, w = _choices(rng, T, E, k)
+    ref, root = np.zeros((T, H)), np.zeros((T, H))
+    for t in range(T):
+        for j in range(k):
+            e = ids[t, j]
+            h = w[t, j] * R.act(x[t] @ g[e], "silu") * (x[t] @ u[e])
+            ref[t] += h @ d[e]
+            root[t] += (h * h) @ (d[e] * d[e])
+    mark(f"outputs round once T{T} E{E} k{k} {H}x{I} {kind}")
+    y = _np(tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down))
+    step = 2.0 ** (np.floor(np.log2(np.abs(ref))) - 7)
+    off = (3e-6 if kind == "bf16" else 9e-6) * np.sqrt(root)
+    allowed = float(np.minimum(off / step, 1.0).sum())
+    assert np.all(np.abs(y - ref) <= 0.5 * step + off + 2.0 ** -8 * off), "one rounding, and what the sums are off by"
+    assert int((y != R.round_bf16(ref)).sum()) <= allowed + 3 * np.sqrt(allowed), (allowed, y.size)

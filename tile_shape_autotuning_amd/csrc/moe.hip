@@ -7,10 +7,11 @@
 //   1. gate and up (moe_up.hip): a workgroup takes a share of one chosen
 //      expert's panels of 16 columns, gate and up together, gathers that
 //      expert's tokens as the rows of its MFMA tiles (panel_stream.hpp) and
-//      writes w * gate(g) * u of each to the workspace, as the sum of two bf16:
-//      16 bits of mantissa, so that the layer rounds once, at y;
-//   2. down (moe_down.hip): the same over the down projection's panels, fp32
-//      sums of each pair of token and expert to the workspace;
+//      writes w * gate(g) * u of each to the workspace, in fp32: the layer
+//      rounds to fewer bits once, at y;
+//   2. down (moe_down.hip): the same over the down projection's panels, whose
+//      rows are those fp32 as three bf16 each, all of their 24 bits; fp32 sums
+//      of each pair of token and expert to the workspace;
 //   3. the sum of each token's pairs, in the order of its choices.
 // No atomics: the same call gives the same bits.
 //
@@ -274,7 +275,7 @@ static MoeParams params_of(int64_t H, int64_t I, int64_t E, int k, const tg_weig
                            void* ws)
 {
     MoeParams p{};
-    p.h = static_cast<unsigned*>(ws);
+    p.h = static_cast<float*>(ws);
     p.up = stack_of(*up, H, I);
     p.down = stack_of(*down, I, H);
     p.stride = ceil_div(I, 16) * 16;
@@ -292,7 +293,7 @@ static int run_mlp(MoeParams p, int64_t T, const void* x, const int32_t* ids, co
     // passes share the workspace: the stream orders them
     for (int64_t t = 0; t < T; t += kTokens) {
         p.T = (int)std::min<int64_t>(kTokens, T - t);
-        p.yp = reinterpret_cast<float*>(p.h + (int64_t)p.T * p.k * p.stride);
+        p.yp = p.h + (int64_t)p.T * p.k * p.stride;
         p.x = static_cast<const unsigned short*>(x) + t * p.H;
         p.ids = ids + t * p.k;
         p.weights = weights + t * p.k;

@@ -38,7 +38,7 @@ struct MoeParams {
     const unsigned short* x;                           // [T][H]
     const int32_t* ids;                                // [T][k]
     const float* weights;
-    unsigned* h;                                       // [T k][stride], two bf16: high half + low half
+    float* h;                                          // [T k][stride]
     float* yp;                                         // [T k][H], each pair's part of y
     unsigned short* y;                                 // [T][H]
     ExpertStack up, down;
@@ -173,8 +173,8 @@ inline int resident_on_cu(Kernel kernel, int threads)
 // rows; `vec`: what is read along it comes in aligned 16 bytes.  Two row tiles
 // where an expert has more than 8 rows on average: with fewer, more than 16
 // are rare, and take a second pass.  Two chunks a wave where eight waves have
-// them.  (16 waves of one chunk: the same within 5 % where there are 16
-// chunks, 33 us instead of 20 where there are 8.)
+// them (F::kMany with two row tiles).  (16 waves of one chunk: the same within
+// 5 % where there are 16 chunks, 33 us instead of 20 where there are 8.)
 template <class F>
 static void by_weight(const tg_weight& w, int64_t K, bool vec, const MoeParams& p, hipStream_t s)
 {
@@ -184,7 +184,7 @@ static void by_weight(const tg_weight& w, int64_t K, bool vec, const MoeParams& 
         constexpr int G = decltype(gs)::value;
         if constexpr (V) {
             if (two) {
-                many ? F::template go<Q, Z, 2, 2, G, V>(p, s) : F::template go<Q, Z, 1, 2, G, V>(p, s);
+                many ? F::template go<Q, Z, 2, F::kMany, G, V>(p, s) : F::template go<Q, Z, 1, 2, G, V>(p, s);
                 return;
             }
         }

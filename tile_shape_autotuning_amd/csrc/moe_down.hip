@@ -8,7 +8,7 @@ namespace tg {
 template <bool W4F, bool ZERO, int MT, int W, int CW, int GS, bool VEC, bool ONE>
 __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p)
 {
-    using S = PanelStream<W4F, ZERO, MT, 1, 2, W, CW, GS, ONE ? 1 : 32>;
+    using S = PanelStream<W4F, ZERO, MT, 1, 3, W, CW, GS, ONE ? 1 : 32>;
     __shared__ f32x4_t red[S::RED], mid[S::MID];
     __shared__ int ids[kTokens * kMaxChoices];
     __shared__ unsigned bits[kExpertWords];
@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p)
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int r = r0 + 16 * m + l16, pair = __shfl(e.pair, r & 63);
-                s.load_pairs(x, m, rh, r < e.rows ? pair * (int)p.stride * 4 : kOOB, (int)p.stride, c0);
+                s.load_floats(x, m, rh, r < e.rows ? pair * (int)p.stride * 4 : kOOB, (int)p.stride, c0);
             }
         };
         auto load = [&](int block, int index, typename S::Words& b, bool some) {
@@ -67,11 +67,14 @@ __global__ void __launch_bounds__(64 * W) moe_down_kernel(MoeParams p)
 }
 
 struct Down {
+    // rows of two tiles and two chunks in three parts do not fit in registers (64
+    // tokens over 8 4-bit experts of 2048 x 1408: 95 us, with one chunk 65)
+    static constexpr int kMany = 1;
     template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
     static void go(MoeParams p, hipStream_t s)
     {
         constexpr int W = 8;
-        using S = PanelStream<W4F, ZERO, MT, 1, 2, W, CW, GS, 32>;
+        using S = PanelStream<W4F, ZERO, MT, 1, 3, W, CW, GS, 32>;
         constexpr size_t used = (S::RED + S::MID) * 16 + (kTokens * kMaxChoices + kExpertWords) * 4;
         static_assert(used + MT * 1024 <= kLdsBytes, "LDS");
         const int slots = std::min(p.E, p.T * p.k);

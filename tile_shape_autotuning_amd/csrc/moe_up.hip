@@ -76,12 +76,7 @@ __global__ void __launch_bounds__(64 * W) moe_up_kernel(MoeParams p)
                 if (row >= e.rows)
                     continue;
                 // columns past I stay zero for the second kernel
-                const float hv = col < p.I ? w * gated(sum[0][r], sum[1][r], p.gelu) : 0.0f;
-                const unsigned short hi = f32_to_bf16_rne(hv);
-                const float rest = hv - __uint_as_float((unsigned)hi << 16);
-                // an infinity or NaN stays one: its rest is no number
-                const unsigned short lo = (hi & 0x7F80u) != 0x7F80u ? f32_to_bf16_rne(rest) : (unsigned short)0;
-                p.h[(int64_t)to * p.stride + col] = (unsigned)hi << 16 | lo;
+                p.h[(int64_t)to * p.stride + col] = col < p.I ? w * gated(sum[0][r], sum[1][r], p.gelu) : 0.0f;
             }
         };
         if constexpr (ONE)
@@ -92,6 +87,7 @@ __global__ void __launch_bounds__(64 * W) moe_up_kernel(MoeParams p)
 }
 
 struct Up {
+    static constexpr int kMany = 2;
     template <bool W4F, bool ZERO, int MT, int CW, int GS, bool VEC>
     static void go(MoeParams p, hipStream_t s)
     {

@@ -180,8 +180,8 @@ struct PanelStream {
                 load_chunk(x.a[i][m][0], row, c0 + i, lane >> 4, K);
         }
     }
-    // Of a row of pairs of bf16, high half the larger (NA = 2): as stored, for settle to part.
-    __device__ __forceinline__ void load_pairs(Rows& x, int m, __amdgpu_buffer_rsrc_t r, int off, int K, int c0) const
+    // Of a row of K fp32 (NA = 3): as stored, for settle to part.
+    __device__ __forceinline__ void load_floats(Rows& x, int m, __amdgpu_buffer_rsrc_t r, int off, int K, int c0) const
     {
 #pragma unroll
         for (int i = 0; i < CW; ++i)
@@ -190,30 +190,45 @@ struct PanelStream {
                 const int k = (c0 + i) * 128 + 32 * t + 8 * (lane >> 4);
                 const int at = off != kOOB && k < K ? off + k * 4 : kOOB;
                 x.a[i][m][0][t] = load16(r, at);
-                x.a[i][m][NA - 1][t] = load16(r, at == kOOB ? kOOB : at + 16);
+                x.a[i][m][1][t] = load16(r, at == kOOB ? kOOB : at + 16);
             }
     }
 
-    // Makes loaded rows ready: parts the pairs, computes the constant sums.
+    // Parts eight fp32, two fragments as loaded, into three fragments of bf16
+    // whose sum they are: each takes the upper half, the sign and eight bits of
+    // mantissa, of what the ones before leave, and 24 bits are three times eight
+    // (but for what lies under 2^-133).  An infinity is its own first part and
+    // leaves nothing.
+    static __device__ __forceinline__ void part(u32x4_t (&a)[NA][4], int t)
+    {
+        const u32x4_t in[2] = {a[0][t], a[1][t]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            unsigned v[2] = {in[e >> 1][e % 2 * 2], in[e >> 1][e % 2 * 2 + 1]};
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                a[n][t][e] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+#pragma unroll
+                for (int q = 0; q < 2 && n < 2; ++q) {
+                    const float x = __uint_as_float(v[q]);
+                    const float rest = x - __uint_as_float(v[q] & 0xFFFF0000u);
+                    v[q] = n > 0 || __builtin_isfinite(x) ? __float_as_uint(rest) : 0u;
+                }
+            }
+        }
+    }
+
+    // Makes loaded rows ready: parts fp32, computes the constant sums.
     __device__ __forceinline__ void settle(Rows& x)
     {
-        if constexpr (NA == 2) {
+        if constexpr (NA == 3) {
 #pragma unroll
             for (int i = 0; i < CW; ++i)
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const u32x4_t p = x.a[i][m][0][t], q = x.a[i][m][1][t];
-                        x.a[i][m][0][t] = u32x4_t{__builtin_amdgcn_perm(p[1], p[0], 0x07060302u),
-                                                  __builtin_amdgcn_perm(p[3], p[2], 0x07060302u),
-                                                  __builtin_amdgcn_perm(q[1], q[0], 0x07060302u),
-                                                  __builtin_amdgcn_perm(q[3], q[2], 0x07060302u)};
-                        x.a[i][m][1][t] = u32x4_t{__builtin_amdgcn_perm(p[1], p[0], 0x05040100u),
-                                                  __builtin_amdgcn_perm(p[3], p[2], 0x05040100u),
-                                                  __builtin_amdgcn_perm(q[1], q[0], 0x05040100u),
-                                                  __builtin_amdgcn_perm(q[3], q[2], 0x05040100u)};
-                    }
+                    for (int t = 0; t < 4; ++t)
+                        part(x.a[i][m], t);
         }
         if constexpr (W4F) {
             const f32x4_t none = {0.f, 0.f, 0.f, 0.f};
