@@ -135,3 +135,26 @@ def test_outputs_round_once(T, E, k, H, I, kind, group, zero):
     allowed = float(np.minimum(off / step, 1.0).sum())
     assert np.all(np.abs(y - ref) <= 0.5 * step + off + 2.0 ** -8 * off), "one rounding, and what the sums are off by"
     assert int((y != R.round_bf16(ref)).sum()) <= allowed + 3 * np.sqrt(allowed), (allowed, y.size)
+
+
+def test_silu_far_from_zero():
+    # A neuron with gate g and one that takes its value away again, to 16 bits of it: y is what is left, 2^-17 of the
+    # value or less, so its rounding to bf16 hides nothing.  SiLU in fp32: exp to a unit (2^-23), a sum and a quotient
+    # to half of one each; the three parts of h and their sums another; u = 2^p and gate(64) = 64 are exact.
+    g = R.round_bf16(-np.concatenate([np.linspace(18.0, 86.5, 40), [0.5, 1.0, 4.0, -3.0, -11.0, -30.0, 17.0, 87.0]]))
+    n = len(g)
+    value = g / (1.0 + np.exp(-g))
+    u = 2.0 ** -np.floor(np.log2(np.abs(value)))
+    take = -value * u / 64.0
+    hi = R.round_bf16(take)
+    mid = R.round_bf16(take - hi)
+    up, down = np.zeros((1, 2, 2 * n, 16)), np.zeros((1, n, 2 * n))
+    up[0, 0, 0::2, 0], up[0, 1, 0::2, 0] = g, u
+    up[0, 0, 1::2, 0], up[0, 1, 1::2, 0], up[0, 1, 1::2, 1] = 64.0, hi, mid
+    down[0, np.arange(n), 2 * np.arange(n)] = down[0, np.arange(n), 2 * np.arange(n) + 1] = 1.0
+    for c in range(0, n, 16):                          # as many outputs as inputs a call
+        y = tg.moe_mlp(torch.ones((1, 16), dtype=torch.bfloat16, device="cuda"), _cuda(np.zeros((1, 1), np.int32)),
+                       torch.ones((1, 1), device="cuda"), _bf16(up), _bf16(down[:, c:c + 16]))
+        ref = (value * u + 64.0 * (hi + mid))[c:c + 16]
+        bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -23 + 3 * 2.0 ** -24) * np.abs(value * u)[c:c + 16]
+        assert np.all(np.abs(_np(y)[0] - ref) <= bound), np.abs(_np(y)[0] - ref) / bound
