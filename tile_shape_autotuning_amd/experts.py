@@ -47,14 +47,25 @@ def _call(name, device, *args):
         _native.check(st)
 
 
+def _group(group, name):
+    # the library takes 32 bits, and ctypes cuts what is longer without a word
+    if group not in (32, 64) and (group < 128 or group % 128 or group >= 2 ** 31):
+        raise ValueError(f"{name}group must be 32, 64 or a multiple of 128 below 2^31")
+
+
+def _int32(v, name):
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} = {v} is out of range")
+    return v
+
+
 def _w4(w, lead, K, N, device, name):
     """tg_weight of a W4 with the leading dimensions `lead`, or the reason it is none."""
     import torch
     words, scales, zeros, wk, wn, group = w
     if (wk, wn) != (K, N):
         raise ValueError(f"{name}: weights are {wk} x {wn}, not {K} x {N}")
-    if group not in (32, 64) and (group < 128 or group % 128):
-        raise ValueError(f"{name}: group must be 32, 64 or a multiple of 128")
+    _group(group, f"{name}: ")
     P, C, G = -(-N // 16), -(-K // 128), -(-K // group)
     if words.dtype != torch.int32 or words.shape != (*lead, P, C, 64, 4):
         raise ValueError(f"{name}: words must be int32 {(*lead, P, C, 64, 4)}")
@@ -90,6 +101,7 @@ def w4_quantize(W, group=128, zero_point=False, scale_dtype=None, values=False):
     that the codes stand for, in W's shape, order and dtype.
     """
     import torch
+    _group(group, "")
     if W.dim() < 2:
         raise ValueError("W must have at least two dimensions")
     if W.dtype not in (torch.bfloat16, torch.float32):
@@ -99,8 +111,6 @@ def w4_quantize(W, group=128, zero_point=False, scale_dtype=None, values=False):
     scale_dtype = scale_dtype or torch.bfloat16
     if scale_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("scale_dtype must be float32 or bfloat16")
-    if group not in (32, 64) and (group < 128 or group % 128):
-        raise ValueError("group must be 32, 64 or a multiple of 128")
     rows_first = W.is_contiguous()
     if not rows_first and not W.transpose(-1, -2).is_contiguous():
         raise ValueError("W, or the transpose of its last two dimensions, must be contiguous")
@@ -149,12 +159,13 @@ def gemm_w4(A, B, bias=None, act="none", out=None, out_dtype=None):
                              or bias.device != dev):
         raise ValueError("bias must be a contiguous float32 [N] tensor on A's device")
     _call("tg_gemm_w4", dev, M, N, K, A.data_ptr(), w, bias.data_ptr() if bias is not None else None, out.data_ptr(),
-          BF16 if out_dtype == torch.bfloat16 else BF16_F32OUT, ACT[act] if isinstance(act, str) else int(act))
+          BF16 if out_dtype == torch.bfloat16 else BF16_F32OUT, ACT[act] if isinstance(act, str) else _int32(int(act), "act"))
     return out
 
 
 def _logits(logits, k):
     import torch
+    _int32(k, "k")
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("logits must be a float32 or bfloat16 [T, E] tensor")
     if not logits.is_cuda or not logits.is_contiguous():
@@ -224,7 +235,7 @@ def moe_mlp(x, ids, weights, gate_up, down, gate="silu", out=None):
     if ids.shape[0] != x.shape[0] or ids.device != x.device or weights.device != x.device or \
             not (ids.is_contiguous() and weights.is_contiguous()):
         raise ValueError("ids and weights must be contiguous, one row for each of x's, on x's device")
-    k = ids.shape[1]
+    k = _int32(ids.shape[1], "k")
     T, H, inter, n, up, dn, out, ws = _experts(x, gate_up, down, None, k, gate, out)
     _call("tg_moe_mlp", x.device, T, H, inter, n, k, x.data_ptr(), ids.data_ptr(), weights.data_ptr(), up, dn,
           out.data_ptr(), GATE[gate], ws.data_ptr(), ws.numel())
