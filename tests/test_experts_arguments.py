@@ -30,3 +30,9 @@ def test_a_number_of_choices_beyond_32_bits_is_refused(k):
         tg.moe_route(torch.zeros((1, 4)), k)
     with pytest.raises(ValueError, match="k ="):
         tg.moe_layer(torch.zeros((1, 64), dtype=torch.bfloat16), torch.zeros((1, 4)), None, None, k)
+
+
+@pytest.mark.parametrize("w", [None, torch.zeros((64, 16)), torch.zeros(6), (1, 2, 3)])
+def test_what_is_no_w4_is_said_to_be_none(w):
+    with pytest.raises(TypeError, match="B must be a W4"):
+        experts._w4(w, (), 64, None, torch.device("cpu"), "B")

@@ -158,3 +158,32 @@ def test_silu_far_from_zero():
         ref = (value * u + 64.0 * (hi + mid))[c:c + 16]
         bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -23 + 3 * 2.0 ** -24) * np.abs(value * u)[c:c + 16]
         assert np.all(np.abs(_np(y)[0] - ref) <= bound), np.abs(_np(y)[0] - ref) / bound
+
+
+# ---------------------------------------------------------------- arguments
+def test_what_is_no_w4_is_refused_by_name():
+    x = torch.ones((4, 64), dtype=torch.bfloat16, device="cuda")
+    ids, w = torch.zeros((4, 1), dtype=torch.int32, device="cuda"), torch.ones((4, 1), device="cuda")
+    up = torch.zeros((2, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    q, _ = _w4(np.random.default_rng(0), (), 64, 32, 32, False, "bf16")
+    for bad in (None, torch.zeros((64, 32), dtype=torch.bfloat16, device="cuda"), q[:5]):
+        with pytest.raises(TypeError, match="B must be a W4"):
+            tg.gemm_w4(x, bad)
+    for bad in (None, q, q[:5]):
+        with pytest.raises(TypeError, match="gate_up must be"):
+            tg.moe_mlp(x, ids, w, bad, torch.zeros((2, 64, 8), dtype=torch.bfloat16, device="cuda"))
+    for bad in (None, q[:5]):
+        with pytest.raises(TypeError, match="down must be"):
+            tg.moe_mlp(x, ids, w, up, bad)
+
+
+def test_a_group_longer_than_the_matrix_is_one_group():
+    rng = np.random.default_rng(41)
+    W = torch.from_numpy(rng.standard_normal((300, 40)).astype(np.float32)).cuda()
+    A = torch.from_numpy(rng.integers(-4, 5, (70, 300)).astype(np.float32)).cuda().to(torch.bfloat16)
+    want, values = tg.w4_quantize(W, 384, zero_point=True, values=True)
+    for group in (2 ** 21, 2 ** 31 - 128):
+        q, v = tg.w4_quantize(W, group, zero_point=True, values=True)
+        assert torch.equal(q.words, want.words) and torch.equal(q.scales, want.scales) and torch.equal(v, values)
+        for M in (1, 40, 70):
+            assert torch.equal(tg.gemm_w4(A[:M], q), tg.gemm_w4(A[:M], want))

@@ -60,9 +60,12 @@ def _int32(v, name):
 
 
 def _w4(w, lead, K, N, device, name):
-    """tg_weight of a W4 with the leading dimensions `lead`, or the reason it is none."""
+    """tg_weight of a W4 with the leading dimensions `lead`, or the reason it is none (N None: as it says)."""
     import torch
+    if w is None or isinstance(w, torch.Tensor) or len(w) != 6:
+        raise TypeError(f"{name} must be a W4: words, scales, zeros, K, N, group")
     words, scales, zeros, wk, wn, group = w
+    N = wn if N is None else N
     if (wk, wn) != (K, N):
         raise ValueError(f"{name}: weights are {wk} x {wn}, not {K} x {N}")
     _group(group, f"{name}: ")
@@ -145,8 +148,8 @@ def gemm_w4(A, B, bias=None, act="none", out=None, out_dtype=None):
         raise ValueError("A must be a contiguous tensor on the GPU")
     M, K = A.shape
     dev = A.device
+    w = _w4(B, (), K, None, dev, "B")
     N = B[4]
-    w = _w4(B, (), K, N, dev, "B")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if out_dtype not in (torch.bfloat16, torch.float32):
@@ -203,6 +206,8 @@ def _experts(x, gate_up, down, E, k, gate, out):
             raise ValueError("gate_up must be [E, 2, I, H]")
         n, inter = gate_up.shape[0], gate_up.shape[2]
     else:
+        if gate_up is None or len(gate_up) != 6 or gate_up[0].dim() != 6:
+            raise TypeError("gate_up must be a bfloat16 [E, 2, I, H] tensor or a W4 with leading dimensions (E, 2)")
         n, inter = gate_up[0].shape[0], gate_up[4]
     if E is not None and n != E:
         raise ValueError(f"gate_up holds {n} experts, logits are for {E}")
