@@ -187,3 +187,64 @@ def test_a_group_longer_than_the_matrix_is_one_group():
         assert torch.equal(q.words, want.words) and torch.equal(q.scales, want.scales) and torch.equal(v, values)
         for M in (1, 40, 70):
             assert torch.equal(tg.gemm_w4(A[:M], q), tg.gemm_w4(A[:M], want))
+
+
+# ---------------------------------------------------------------- hot experts
+def _skewed(rng, T, E, k, hot):
+    """Every token names expert `hot` first, the others are spread over the rest."""
+    rest = np.array([e for e in range(E) if e != hot])
+    ids = np.stack([np.concatenate([[hot], rng.permutation(rest)[:k - 1]]) for _ in range(T)]).astype(np.int32)
+    for row in ids:
+        rng.shuffle(row)
+    return ids, (rng.integers(1, 9, (T, k)) / 8.0).astype(np.float32)
+
+
+def _check_close(y, x, ids, w, g, u, d, act):
+    """Against the oracle in norms, token by token: g and u are exact, h is off by 2^-22 (exp, sum, quotient, product),
+    the last sums by at most 48 + 4 blocks of fp32 additions of partial sums up to the root of their terms' squares (in
+    4 bits 3.2 times that, see test_outputs_round_once), and one rounding to bf16 of half a step, 2^-8 of the value."""
+    ref, root, d2 = np.zeros(y.shape), np.zeros(y.shape), d * d
+    for t in range(len(x)):
+        for j in range(ids.shape[1]):
+            if 0 <= ids[t, j] < len(g):
+                e = ids[t, j]
+                h = w[t, j].astype(np.float64) * R.act(x[t] @ g[e], act) * (x[t] @ u[e])
+                ref[t] += h @ d[e]
+                root[t] += (h * h) @ d2[e]
+    size = np.sqrt(root.sum(1))
+    off = np.linalg.norm(_np(y) - ref, axis=1)
+    assert np.all(off <= 2.0 ** -8 * np.linalg.norm(ref, axis=1) + 1e-5 * size), off / size
+
+
+# (T, E, k, H, I, kind): whether there is one row tile (T k <= 8 E), and how many panels and blocks a workgroup has
+HOT = [(64, 64, 2, 256, 128, "bf16"), (64, 64, 2, 256, 128, "w4"),
+       # several blocks of both reductions, several panels a workgroup
+       (40, 48, 2, 2200, 2100, "w4"), (33, 40, 2, 2200, 2304, "bf16"),
+       # one panel a workgroup, one expert: next block's rows on their way with its words
+       (20, 64, 1, 4104, 64, "w4"), (20, 64, 1, 4104, 64, "bf16"), (20, 64, 1, 64, 4104, "w4"),
+       (20, 64, 1, 64, 4104, "bf16"),
+       # two row tiles, more than 32 rows, several blocks
+       (64, 2, 2, 2200, 1300, "w4"), (50, 3, 2, 2200, 1300, "bf16"), (64, 8, 8, 136, 72, "w4"),
+       # the element-load forms
+       (64, 64, 2, 1101, 1277, "bf16"), (40, 2, 2, 1101, 1277, "bf16"), (40, 48, 2, 1101, 1277, "w4")]
+
+
+@pytest.mark.parametrize("T,E,k,H,I,kind", HOT)
+def test_a_hot_expert_takes_several_passes(T, E, k, H, I, kind):
+    rng = np.random.default_rng(T + H + I)
+    some = E if E * H * I < 2 ** 24 else 3             # distinct experts; the others repeat them
+    up, down, g, u, d = _experts(rng, some, H, I, kind)
+    pick = np.arange(E) % some
+    at = torch.from_numpy(pick).cuda()
+    if kind == "w4":
+        up, down = (tg.W4(q.words[at], q.scales[at], q.zeros[at], *q[3:]) for q in (up, down))
+    else:
+        up, down = up[at], down[at]
+    x = rng.integers(-2, 3, (T, H)).astype(np.float64)
+    ids, w = _skewed(rng, T, E, k, E // 3)
+    mark(f"hot expert T{T} E{E} k{k} H{H} I{I} {kind} row tiles {1 if T <= 16 or T * k <= 8 * E else 2}")
+    y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down)
+    again = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down)
+    torch.cuda.synchronize()
+    assert torch.equal(y, again)
+    _check_close(y, x, pick[ids], w, g, u, d, "silu")
