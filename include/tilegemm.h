@@ -496,8 +496,11 @@ int tg_moe_route(int64_t T, int64_t E, int k, const void *logits, int dtype, int
  * elsewhere); an expert that a token names twice counts with both weights; a
  * token without experts gets zeros.  workspace: device memory of
  * tg_moe_workspace_bytes(T, H, I, k), 16-byte aligned, not shared by calls that
- * may overlap.  y must not overlap the inputs.  Tokens are taken 64 at a time: every 64 read the experts that
- * they chose once.  The same call gives the same bits.
+ * may overlap.  y must not overlap the inputs.  Tokens are taken in passes of
+ * up to 64.  A pass of n tokens reads an expert's weights once for each 16 of
+ * the tokens that chose it, or for each 32 where n > 16 and n k > 8 E: a few
+ * tokens read the experts that they chose once, skewed choices read a hot
+ * expert up to four times.  The same call gives the same bits.
  * Limits: H, I <= 65536 and those of tg_moe_route (TG_E_UNSUPPORTED).
  */
 int tg_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int k, size_t *bytes);

@@ -3,7 +3,8 @@
 // with bf16 weights stored [out][in], or 4-bit weights (w4.hpp).
 //
 // A few tokens choose a few rows for each expert: the work is the stream of the
-// chosen experts' weights, each read once.  Three kernels:
+// chosen experts' weights, each read once for 16 rows, or 32 where experts have
+// more than 8 on average (moe.hpp).  Three kernels:
 //   1. gate and up (moe_up.hip): a workgroup takes a share of one chosen
 //      expert's panels of 16 columns, gate and up together, gathers that
 //      expert's tokens as the rows of its MFMA tiles (panel_stream.hpp) and

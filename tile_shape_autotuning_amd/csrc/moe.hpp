@@ -172,9 +172,10 @@ inline int resident_on_cu(Kernel kernel, int threads)
 // F::go<W4F, ZERO, MT, CW, GS, VEC>(p, s) for a weight whose reduction has K
 // rows; `vec`: what is read along it comes in aligned 16 bytes.  Two row tiles
 // where an expert has more than 8 rows on average: with fewer, more than 16
-// are rare, and take a second pass.  Two chunks a wave where eight waves have
-// them (F::kMany with two row tiles).  (16 waves of one chunk: the same within
-// 5 % where there are 16 chunks, 33 us instead of 20 where there are 8.)
+// are rare, and their panels stream by once more for each 16.  Two chunks a
+// wave where eight waves have them (F::kMany with two row tiles).  (16 waves of
+// one chunk: the same within 5 % where there are 16 chunks, 33 us instead of 20
+// where there are 8.)
 template <class F>
 static void by_weight(const tg_weight& w, int64_t K, bool vec, const MoeParams& p, hipStream_t s)
 {

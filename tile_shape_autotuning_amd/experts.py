@@ -231,8 +231,9 @@ def moe_mlp(x, ids, weights, gate_up, down, gate="silu", out=None):
     gate_up: bfloat16 [E, 2, I, H] (gate, up) or a W4 with leading dimensions
     (E, 2), K = H, N = I; down: bfloat16 [E, H, I] or a W4 with leading
     dimension (E,), K = I, N = H; gate: "silu" | "gelu".  ids outside [0, E)
-    add nothing.  Every 64 tokens read the experts that they chose once.
-    Returns y [T, H] bfloat16.
+    add nothing.  Tokens are taken in passes of up to 64; a pass of n reads an
+    expert's weights once for each 16 of its tokens that chose the expert (for
+    each 32 where n > 16 and n k > 8 E).  Returns y [T, H] bfloat16.
     """
     import torch
     if ids.dim() != 2 or ids.dtype != torch.int32 or weights.dtype != torch.float32 or weights.shape != ids.shape:
