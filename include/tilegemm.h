@@ -468,8 +468,12 @@ int tg_w4_quantize(int64_t count, int64_t K, int64_t N, int group, const void *W
  * C = act(A . B + bias), B in 4 bits (TG_W_W4): A bf16 M x K, C M x N bf16 or
  * fp32 (dtype = TG_BF16 or TG_BF16_F32OUT), both row-major, element alignment;
  * bias N floats or NULL; act a tg_act.  K >= 1.  Sums are fp32; the weights'
- * values enter the sums unrounded.  C must not overlap the inputs.  A row of A
- * that holds an infinity gives NaN.
+ * values enter the sums unrounded.  C must not overlap the inputs.
+ * Range: let S be the largest sum of |A| over 128 consecutive k (from a multiple
+ * of 128) of a row.  A row holds the formula where S max(1, scale) <= 2^123
+ * (1e37; elements up to 8e34 always do).  Above, the constant parts of its sums,
+ * up to 31 S, may overflow and give NaN where the formula is finite; a row
+ * that holds an infinity gives NaN.  Other rows are not affected.
  * Limits: K, N <= 2^21, M <= 2^20 (TG_E_UNSUPPORTED).
  */
 int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void *A, const tg_weight *B, const float *bias, void *C,
@@ -500,7 +504,10 @@ int tg_moe_route(int64_t T, int64_t E, int k, const void *logits, int dtype, int
  * up to 64.  A pass of n tokens reads an expert's weights once for each 16 of
  * the tokens that chose it, or for each 32 where n > 16 and n k > 8 E: a few
  * tokens read the experts that they chose once, skewed choices read a hot
- * expert up to four times.  The same call gives the same bits.
+ * expert up to four times.  The same call gives the same bits.  The gated
+ * intermediate is fp32.  4-bit gate_up holds x[t], and 4-bit down holds
+ * weight * gate * up, to the range of A in tg_gemm_w4; bf16 experts have the
+ * range of fp32.
  * Limits: H, I <= 65536 and those of tg_moe_route (TG_E_UNSUPPORTED).
  */
 int tg_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int k, size_t *bytes);

@@ -248,3 +248,38 @@ def test_a_hot_expert_takes_several_passes(T, E, k, H, I, kind):
     torch.cuda.synchronize()
     assert torch.equal(y, again)
     _check_close(y, x, pick[ids], w, g, u, d, "silu")
+
+
+# ---------------------------------------------------------------- the range of 4-bit products
+@pytest.mark.parametrize("M", [1, 20, 40, 130])
+@pytest.mark.parametrize("group,zero", [(128, False), (128, True), (64, False), (64, True), (32, True), (32, False)])
+def test_gemm_w4_up_to_the_end_of_its_range(M, group, zero):
+    # integers times 2^114: sums of |A| over 128 k up to 128 * 4 * 2^114 = 2^123, the largest held; a power of two
+    # changes no rounding, so exact integers stay exact
+    rng = np.random.default_rng(M + group)
+    K, N, far = 712, 72, 2.0 ** 114
+    A = rng.integers(-4, 5, (M, K)).astype(np.float64)
+    A[0], A[M // 2] = 4.0, -4.0
+    q, W = _w4(rng, (), K, N, group, zero, "f32", powers=(0.5 / far, 1.0 / far, 2.0 / far))
+    C = tg.gemm_w4(_bf16(A * far), q, out_dtype=torch.float32)
+    assert np.array_equal(_np(C), (A * far) @ W)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("group,zero", [(128, False), (64, True), (32, True)])
+def test_4_bit_experts_up_to_the_end_of_their_range(T, group, zero):
+    # x and the hidden state times a power of two, the weights' scales divided by it: the same bits
+    rng = np.random.default_rng(T + group)
+    E, k, H, I, far = 2, 2, 200, 136, 2.0 ** 114
+    up, down, g, u, d = _experts(rng, E, H, I, "w4", group, zero, "f32")
+    x = rng.integers(-4, 5, (T, H)).astype(np.float64)
+    x[0] = 4.0
+    ids, w = _choices(rng, T, E, k)
+    want = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down)
+    y = tg.moe_mlp(_bf16(x * far), _cuda(ids), _cuda(w), up._replace(scales=up.scales / far), down)
+    assert torch.equal(y, want)
+    h = np.max(np.abs(np.stack([R.act(x @ g[e], "silu") * (x @ u[e]) for e in range(E)])).sum(2))
+    far = 2.0 ** (122 - np.ceil(np.log2(h)))           # times weights up to 1: half of the range
+    y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda((w * far).astype(np.float32)), up,
+                   down._replace(scales=down.scales / np.float32(far)))
+    assert torch.equal(y, want) and bool(torch.isfinite(y).all())

@@ -21,8 +21,9 @@
 // Products of two bf16 are exact in fp32.  The second and third brackets do
 // not depend on the column: they are MFMAs against constant operands, shared
 // by every panel that a wave works on.  (An offset of 128, the mantissa's low
-// bits, would save a shift and cost 8x the cancellation.)  A row of A that
-// holds an infinity gives NaN.
+// bits, would save a shift and cost 8x the cancellation.)  Partial sums of a
+// chunk reach 31 S, S the sum of |A| over its k: up to S = 2^123 nothing
+// overflows.  A row of A beyond, or with an infinity, gives NaN.
 #pragma once
 
 #include <hip/hip_runtime.h>

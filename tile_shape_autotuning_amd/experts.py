@@ -139,7 +139,8 @@ def gemm_w4(A, B, bias=None, act="none", out=None, out_dtype=None):
     A: [M, K] bfloat16, contiguous; B: a W4 without leading dimensions; bias:
     [N] float32 or None; act: "none" | "relu" | "gelu"; out_dtype:
     torch.bfloat16 (default) or torch.float32.  Runs on the current stream and
-    returns C.
+    returns C.  Rows of A whose elements stay below 8e34 never overflow on the
+    way; what larger ones give is in tilegemm.h.
     """
     import torch
     if A.dim() != 2 or A.dtype != torch.bfloat16:
