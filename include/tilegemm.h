@@ -449,13 +449,13 @@ typedef enum {
  * scales and zeros as above for each; zeros NULL: symmetric codes.  values
  * (may be NULL): what the codes stand for, in W's order and type.
  *   symmetric:  scale = round(max |w| / 7) over the group, zero point 8
- *   zeros:      lo = min(w, 0), hi = max(w, 0), scale = round((hi - lo) / 15),
+ *   zeros:      lo = min(w, 0), hi = max(w, 0), scale = round(fp32(hi - lo) / 15),
  *               zero = clamp(rint(-lo / scale), 0, 15)
  *   code        = clamp(rint(w / scale) + zero, 0, 15)
  * round is to fp32, then to scale_dtype; rint of the exact quotient, ties to
  * even.  A group whose scale is zero has codes that stand for zero; one that
- * holds an infinity or NaN, or whose range overflows fp32, has values that
- * are NaN.  Storage past K and N is written as zero.  The outputs must not
+ * holds an infinity or NaN, or whose range overflows fp32, has NaN as its scale
+ * and for values.  Storage past K and N is written as zero.  The outputs must not
  * overlap W.  Asynchronous on the stream of tg_set_stream, as are all
  * functions of this section; none of them allocates, so each may be captured
  * into a graph.  Bad arguments are TG_E_INVAL, before anything is queued.

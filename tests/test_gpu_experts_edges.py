@@ -283,3 +283,25 @@ def test_4_bit_experts_up_to_the_end_of_their_range(T, group, zero):
     y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda((w * far).astype(np.float32)), up,
                    down._replace(scales=down.scales / np.float32(far)))
     assert torch.equal(y, want) and bool(torch.isfinite(y).all())
+
+
+# ---------------------------------------------------------------- quantisation
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", ["f32", "bf16"])
+def test_a_range_that_overflows_gives_nan_in_products_too(scale, dtype):
+    W = torch.ones((160, 3), device="cuda")
+    W[3, 0], W[4, 0] = 3e38, -3e38                     # hi - lo overflows fp32
+    W[3, 1] = 3e38                                     # large, but no overflow
+    if dtype == "bf16":
+        W = W.to(torch.bfloat16)
+    q, v = tg.w4_quantize(W, 64, zero_point=True, scale_dtype=torch.float32 if scale == "f32" else None, values=True)
+    nan = torch.isnan(v).cpu()
+    assert bool(nan[:64, 0].all()) and int(nan.sum()) == 64
+    assert int(torch.isnan(q.scales).sum()) == 1 and not bool(torch.isinf(q.scales).any())
+    A = torch.randn((70, 160), device="cuda").to(torch.bfloat16) * 2.0 ** -10      # S times 2e37 is in range
+    for M in (1, 20, 70):
+        C = tg.gemm_w4(A[:M], q, out_dtype=torch.float32)
+        assert bool(torch.isnan(C[:, 0]).all()) and bool(torch.isfinite(C[:, 1:]).all())
+    # symmetric: no overflow, the largest magnitude is a code
+    s, v = tg.w4_quantize(W, 64, values=True)
+    assert bool(torch.isfinite(s.scales).all()) and bool(torch.isfinite(v).all())

@@ -2,7 +2,8 @@
 // point, for every group of rows of a column.
 //
 //   symmetric:   s = round(max |w| / 7),  z = 8
-//   zero point:  lo = min(w, 0), hi = max(w, 0) over the group,
+//   zero point:  lo = min(w, 0), hi = max(w, 0) over the group, hi - lo
+//                rounded to fp32,
 //                s = round((hi - lo) / 15),  z = clamp(rint(-lo / s), 0, 15)
 //   code         q = clamp(rint(w / s) + z, 0, 15)
 // where round() is to fp32 and then to the scales' type.  The quotients are
@@ -206,7 +207,9 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(QuantParams p)
         z[t] = 8.0f;
         if (p.zero)
             z[t] = usable ? fminf(exact_quotient(-lo[t] * up[t], su[t], rintf(-lo[t] * up[t] * inv[t])), 15.0f) : 0.0f;
-        if (bad)
+        // a group that is not finite, or whose range is not: an infinite scale
+        // times a code's distance of zero, or of nearly zero in a product's sums
+        if (bad || s[t] == INFINITY)
             s[t] = NAN;
     }
     // scales and zero points: one lane a column and group; columns past N hold zero
