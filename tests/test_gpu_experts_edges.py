@@ -305,3 +305,41 @@ def test_a_range_that_overflows_gives_nan_in_products_too(scale, dtype):
     # symmetric: no overflow, the largest magnitude is a code
     s, v = tg.w4_quantize(W, 64, values=True)
     assert bool(torch.isfinite(s.scales).all()) and bool(torch.isfinite(v).all())
+
+
+# ---------------------------------------------------------------- shares of the work
+@pytest.mark.parametrize("cus", [1, 7, 304, 2 ** 31 - 1])
+def test_shares_follow_the_device_description(cus):
+    # More or fewer panels a workgroup: blocks of the reduction meet wave by wave or, with one panel, at the end, so
+    # the same products are added in another order.  Either order is off by at most 136 additions in a group and
+    # one a chunk or block, 2^-23 each of terms of up to 63 scales (test_gemm_w4_on_random_rows), before the
+    # rounding to bf16, whose results are then a step (2^-7) apart at most.  g and u come in one block: the same bits.
+    rng = np.random.default_rng(cus % 1000)
+    q, W = _w4(rng, (), 2200, 700, 64, True, "bf16")
+    up, down, g, u, d = _experts(rng, 5, 264, 2200, "w4")
+    x = torch.randn((200, 2200), device="cuda").to(torch.bfloat16)
+    rows = torch.randn((30, 264), device="cuda").to(torch.bfloat16)
+    choice, share = _choices(rng, 30, 5, 2)
+    ids, w = _cuda(choice), _cuda(share)
+
+    def everything():
+        return [tg.gemm_w4(x[:M], q) for M in (3, 30, 60, 200)] + \
+            [tg.moe_mlp(rows[:T], ids[:T], w[:T], up, down) for T in (2, 30)]
+
+    want = everything()
+    desc = tg.get_device_desc()
+    desc.n_cu = cus
+    tg.set_device_override(desc)
+    try:
+        got = everything()
+    finally:
+        tg.set_device_override(None)
+    size = np.abs(_np(x)) @ np.full((2200, 700), 63.0 * 2.0)
+    _, terms = R.mlp(_np(rows), choice, share.astype(np.float64), g, u, d, "silu")
+    terms *= np.max(np.abs(d)) / np.mean(np.abs(d)) * 63.0 * 1.01
+    for a, b in zip(got, want):
+        a, b = _np(a), _np(b)
+        most = 2 * (136 + 18 + 18) * 2.0 ** -23 * (size if a.shape[1] == 700 else terms)[:len(a)]
+        assert np.all(np.abs(a - b) <= 2.0 ** -7 * np.maximum(np.abs(a), np.abs(b)) + most)
+    for a, b in zip(got[:4], want[:4]):
+        assert np.linalg.norm(_np(a) - _np(b)) <= 2.0 ** -8 * np.linalg.norm(_np(b))

@@ -436,7 +436,8 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
     // 28.5, 4 for 448 40 (two thirds of which start when others end); 16 waves
     // of 2 chunks 26.7, 8 of 4 28.6, 8 of 2 31.6.  With more rows A's fragments
     // leave room for fewer waves.
-    const int per = (int)ceil_div(p.panels, kCus);
+    const int64_t cus = compute_units();
+    const int per = (int)ceil_div(p.panels, cus);
     if (M <= 16)
         return p.w.chunks <= 16 ? launch_panels<1, 16, 1>(p, per, s) : launch_panels<1, 16, 2>(p, per, s);
     if (M <= 32)
@@ -447,9 +448,9 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
     // one has, else 64 x 64: 2048 x 4096 x 4096 77, 85 and 112 us, 100 x 28672 x
     // 4096 59, 50 and 66, 128 x 4096 x 4096 58, 38 and 30.  (128 x 256 leaves
     // one workgroup a compute unit: 151 us for the first.)
-    if (ceil_div(M, 64) * ceil_div(p.panels, 16) >= 2 * kCus)
+    if (ceil_div(M, 64) * ceil_div(p.panels, 16) >= 2 * cus)
         return launch_tiled<4, 4>(p, s);
-    if (ceil_div(M, 64) * ceil_div(p.panels, 8) >= kCus)
+    if (ceil_div(M, 64) * ceil_div(p.panels, 8) >= cus)
         return launch_tiled<4, 2>(p, s);
     return launch_tiled<4, 1>(p, s);
 }

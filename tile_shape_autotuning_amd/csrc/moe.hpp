@@ -150,8 +150,8 @@ inline int panels_per(int panels, const MoeParams& p, int resident, int blocks, 
 {
     const double miss = 1.0 - (double)p.k / p.E;
     const double chosen = std::min<double>((double)p.T * p.k, p.E * (1.0 - std::pow(miss, p.T)));
-    const int each = std::max(1, (int)((double)kCus * resident / std::max(1.0, chosen)));
-    int64_t per = ceil_div(panels, std::min(each, panels));
+    const double each = (double)compute_units() * resident / std::max(1.0, chosen);
+    int64_t per = ceil_div(panels, std::max(1, (int)std::min<double>(each, panels)));
     if (blocks > 1)
         per = std::min<int64_t>(per, (int64_t)((kLdsBytes - used) / panel_bytes));
     return (int)std::min<int64_t>(per, panels_in_reach((std::max(p.H, p.I) + 127) / 128));

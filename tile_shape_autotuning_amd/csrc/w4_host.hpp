@@ -9,9 +9,11 @@
 namespace tg {
 
 constexpr size_t kLdsBytes = 160 * 1024;       // of a workgroup on gfx950
-constexpr int kCus = 256;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Compute units to share the work among: of the device description in force.
+inline int64_t compute_units() { return current_desc().n_cu; }
 
 // TG_OK, or the error (set) that a call reports for weight `name`.
 int check_weight(const tg_weight* w, const char* name);
