@@ -33,16 +33,15 @@ class W4(NamedTuple):
     group: int
 
 
-def _call(name, device, *args):
-    """Calls the library on `device` and its current stream; raises what the library refuses."""
+def _call(entry, device, *args):
+    """Calls an entry point of the library on `device` and its current stream; raises what the library refuses."""
     import torch
     index = device.index
     if index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _call(name, device, *args)
-    L = _native.lib()
-    L.tg_set_stream(torch._C._cuda_getCurrentRawStream(index))
-    st = getattr(L, name)(*args)
+            return _call(entry, device, *args)
+    _native.lib().tg_set_stream(torch._C._cuda_getCurrentRawStream(index))
+    st = entry(*args)
     if st:
         _native.check(st)
 
@@ -126,8 +125,8 @@ def w4_quantize(W, group=128, zero_point=False, scale_dtype=None, values=False):
     scales = torch.empty((*lead, P, G, 16), dtype=scale_dtype, device=dev)
     zeros = torch.empty((*lead, P, G, 16), dtype=torch.uint8, device=dev) if zero_point else None
     out = torch.empty_like(W) if values else None      # keeps W's order
-    _call("tg_w4_quantize", dev, lead.numel(), K, N, group, W.data_ptr(), F32 if W.dtype == torch.float32 else BF16,
-          rows_first, F32 if scale_dtype == torch.float32 else BF16, words.data_ptr(), scales.data_ptr(),
+    _call(_native.w4_quantize_ptr, dev, lead.numel(), K, N, group, W.data_ptr(),
+          F32 if W.dtype == torch.float32 else BF16, rows_first, F32 if scale_dtype == torch.float32 else BF16, words.data_ptr(), scales.data_ptr(),
           zeros.data_ptr() if zero_point else None, out.data_ptr() if values else None)
     q = W4(words, scales, zeros, K, N, group)
     return (q, out) if values else q
@@ -162,8 +161,9 @@ def gemm_w4(A, B, bias=None, act="none", out=None, out_dtype=None):
     if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_contiguous()
                              or bias.device != dev):
         raise ValueError("bias must be a contiguous float32 [N] tensor on A's device")
-    _call("tg_gemm_w4", dev, M, N, K, A.data_ptr(), w, bias.data_ptr() if bias is not None else None, out.data_ptr(),
-          BF16 if out_dtype == torch.bfloat16 else BF16_F32OUT, ACT[act] if isinstance(act, str) else _int32(int(act), "act"))
+    _call(_native.gemm_w4_ptr, dev, M, N, K, A.data_ptr(), w, bias.data_ptr() if bias is not None else None,
+          out.data_ptr(), BF16 if out_dtype == torch.bfloat16 else BF16_F32OUT,
+          ACT[act] if isinstance(act, str) else _int32(int(act), "act"))
     return out
 
 
@@ -190,8 +190,8 @@ def moe_route(logits, k, renorm=True):
     import torch
     ids, weights = _logits(logits, k)
     T, E = logits.shape
-    _call("tg_moe_route", logits.device, T, E, k, logits.data_ptr(), F32 if logits.dtype == torch.float32 else BF16,
-          bool(renorm), ids.data_ptr(), weights.data_ptr())
+    _call(_native.moe_route_ptr, logits.device, T, E, k, logits.data_ptr(),
+          F32 if logits.dtype == torch.float32 else BF16, renorm, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -244,7 +244,7 @@ def moe_mlp(x, ids, weights, gate_up, down, gate="silu", out=None):
         raise ValueError("ids and weights must be contiguous, one row for each of x's, on x's device")
     k = _int32(ids.shape[1], "k")
     T, H, inter, n, up, dn, out, ws = _experts(x, gate_up, down, None, k, gate, out)
-    _call("tg_moe_mlp", x.device, T, H, inter, n, k, x.data_ptr(), ids.data_ptr(), weights.data_ptr(), up, dn,
+    _call(_native.moe_mlp_ptr, x.device, T, H, inter, n, k, x.data_ptr(), ids.data_ptr(), weights.data_ptr(), up, dn,
           out.data_ptr(), GATE[gate], ws.data_ptr(), ws.numel())
     return out
 
@@ -256,7 +256,7 @@ def moe_layer(x, logits, gate_up, down, k, renorm=True, gate="silu", out=None):
     if logits.shape[0] != x.shape[0] or logits.device != x.device:
         raise ValueError("logits must have one row for each of x's, on x's device")
     T, H, inter, n, up, dn, out, ws = _experts(x, gate_up, down, logits.shape[1], k, gate, out)
-    _call("tg_moe_layer", x.device, T, H, inter, n, k, x.data_ptr(), logits.data_ptr(),
-          F32 if logits.dtype == torch.float32 else BF16, bool(renorm), up, dn, out.data_ptr(), ids.data_ptr(),
+    _call(_native.moe_layer_ptr, x.device, T, H, inter, n, k, x.data_ptr(), logits.data_ptr(),
+          F32 if logits.dtype == torch.float32 else BF16, renorm, up, dn, out.data_ptr(), ids.data_ptr(),
           weights.data_ptr(), GATE[gate], ws.data_ptr(), ws.numel())
     return out, ids, weights
