@@ -40,7 +40,8 @@ def _pair_columns(rng, E, I, H, at):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
-@pytest.mark.parametrize("kind,group,zero", [("bf16", 0, False), ("w4", 128, False), ("w4", 64, True), ("w4", 32, True)])
+@pytest.mark.parametrize("kind,group,zero", [("bf16", 0, False), ("w4", 128, False), ("w4", 64, True),
+                                             ("w4", 32, True)])
 @pytest.mark.parametrize("T,E,I", [(3, 2, 520), (2, 2, 2600), (40, 2, 520), (40, 2, 1300), (40, 2, 2600), (3, 2, 301)])
 def test_hidden_values_keep_24_bits(T, E, I, kind, group, zero, act):
     # h <= 700^2 < 2^24 / 31, alone in its chunk: every sum, the 4-bit product's constant parts (31 h, 24 h)

@@ -155,13 +155,17 @@ static int launch_panels(GemmW4Params p, int per, hipStream_t s)
 // transfers straight from memory, three stages).  W's codes are a quarter of
 // A's bytes, so tiles are wide rather than tall, and no two waves expand the
 // same codes: with MT = NT = 4, 144 expanding instructions a chunk beside 64
-// MFMAs and 64 FMAs of the scales.  The sums that do not depend on the column
+// MFMAs, 64 FMAs of the scales and as many copies of the starting sums.  The sums that do not depend on the column
 // (w4.hpp) are computed one chunk ahead, each wave a quarter of the rows, and
 // start the accumulators.  One barrier a chunk; it and the transfers are
 // covered by the other workgroups of the compute unit (two of 256 registers
-// with NT = 4, three with NT = 2).  Bound by issue: 2048 x 4096 x 4096 75 us, 0.9
-// PFLOP/s (zero points 93; groups of 64 86 and 141, of 32 103 and 141); 4096 x
-// 8192 x 8192 501 us, 1.1 PFLOP/s.
+// with NT = 4, three with NT = 2).  Calls back to back: 2048 x 4096 x 4096 78 to
+// 85 us, 0.85 PFLOP/s (zero points 98; groups of 64 91 and 143, of 32 107 and
+// 142; K one less, through registers, 117); 4096 x 8192 x 8192 580 us, 0.95
+// PFLOP/s.  By counters the first keeps the matrix cores busy 42 % of the time
+// and the vector units 50 % with what is beside them (324 instructions and 68
+// MFMAs a wave and chunk): two waves a SIMD hide little of one behind the
+// other, and wait for the chunk's transfers and its barrier 23 % of theirs.
 //
 // Stage layout: row r of A, 256 bytes, 16-byte piece q at q ^ swz<16>(r): the
 // 16 rows of a fragment read hit 16 different pieces.
@@ -445,9 +449,14 @@ extern "C" int tg_gemm_w4(int64_t M, int64_t N, int64_t K, const void* A, const 
     if (M <= 64)
         return p.w.chunks <= 8 ? launch_panels<4, 8, 1>(p, per, s) : launch_panels<4, 8, 2>(p, per, s);
     // 64 x 256 tiles where two workgroups a compute unit have one, 64 x 128 where
-    // one has, else 64 x 64: 2048 x 4096 x 4096 77, 85 and 112 us, 100 x 28672 x
-    // 4096 59, 50 and 66, 128 x 4096 x 4096 58, 38 and 30.  (128 x 256 leaves
-    // one workgroup a compute unit: 151 us for the first.)
+    // one has, else 64 x 64.  Symmetric groups of 128 in the three: 2048 x 4096 x
+    // 4096 86, 95 and 126 us, 512 x 4096 x 4096 53, 37 and 39, 100 x 28672 x 4096
+    // 54, 48 and 67, 128 x 4096 x 4096 52, 35 and 30; groups of 32 with zero
+    // points 143, 179 and 261, 111, 82 and 87, 112, 98 and 166, 112, 81 and 77.
+    // At eight shapes in all six storage forms the rule's tile is within 6 % of
+    // the best, but where the widest just misses two workgroups (256 x 28672 x
+    // 4096, 448 tiles: 79 and 89 us, groups of 32 with zero points 142 and 182).
+    // (128 x 256 leaves one workgroup a compute unit: 151 us for the first.)
     if (ceil_div(M, 64) * ceil_div(p.panels, 16) >= 2 * cus)
         return launch_tiled<4, 4>(p, s);
     if (ceil_div(M, 64) * ceil_div(p.panels, 8) >= cus)

@@ -22,10 +22,11 @@
 // with the sum of both weights.
 //
 // Bound by the stream: two of eight bf16 experts of 4096 x 14336 for one token
-// 84 + 50 + 4 us, 5.6 and 4.7 TB/s in the first two; 64 tokens over 64 experts
-// of 2048 x 1408 in 4 bits 50 + 38 + 5 us, 3.7 and 2.4 TB/s (the expanding and
-// multiplying of six rows an expert takes 8 us of the 38, the meeting of the
-// sums 5, and 11 chunks leave two of eight waves without a load).
+// 82 + 54 + 5 us, 5.8 and 4.4 TB/s in the first two; 64 tokens over 64 experts
+// of 2048 x 1408 in 4 bits 52 + 45 + 5 us, 3.9 and 2.2 TB/s (in the second, the
+// third part of the hidden state takes 6 us, the expanding and the other two
+// products 8, the meeting of the sums 5, and 11 chunks leave two of eight waves
+// without a load).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -14,9 +14,10 @@
 // the others go on in the other half of the buffer.  For 16 rows of 28672 x
 // 8192 in 4 bits: loads of a panel for every wave's own A 79 us, rows kept and
 // panels streamed 42, scales left as loaded until their step 30, a barrier for
-// four panels and the next block's words ahead 27 (31 with zero points, 4.0
-// TB/s; what is left over the 24 us of a copy is the start of the stream, the
-// meeting of the sums and 36 VALU instructions a KiB of codes).
+// four panels and the next block's words ahead 27 on that day's card, 31 on
+// others (with zero points 31 to 34, 3.6 to 4.0 TB/s).  What is left over the 24
+// us of a copy is the start of the stream, the meeting of the sums and 36 VALU
+// instructions a KiB of codes.
 //
 // The constant parts of the 4-bit sums (the two brackets of w4.hpp that do not
 // depend on the column) are computed once for each chunk when the fragments

@@ -126,8 +126,8 @@ def w4_quantize(W, group=128, zero_point=False, scale_dtype=None, values=False):
     zeros = torch.empty((*lead, P, G, 16), dtype=torch.uint8, device=dev) if zero_point else None
     out = torch.empty_like(W) if values else None      # keeps W's order
     _call(_native.w4_quantize_ptr, dev, lead.numel(), K, N, group, W.data_ptr(),
-          F32 if W.dtype == torch.float32 else BF16, rows_first, F32 if scale_dtype == torch.float32 else BF16, words.data_ptr(), scales.data_ptr(),
-          zeros.data_ptr() if zero_point else None, out.data_ptr() if values else None)
+          F32 if W.dtype == torch.float32 else BF16, rows_first, F32 if scale_dtype == torch.float32 else BF16,
+          words.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zero_point else None, out.data_ptr() if values else None)
     q = W4(words, scales, zeros, K, N, group)
     return (q, out) if values else q
 
