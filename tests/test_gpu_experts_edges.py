@@ -344,3 +344,95 @@ def test_shares_follow_the_device_description(cus):
         assert np.all(np.abs(a - b) <= 2.0 ** -7 * np.maximum(np.abs(a), np.abs(b)) + most)
     for a, b in zip(got[:4], want[:4]):
         assert np.linalg.norm(_np(a) - _np(b)) <= 2.0 ** -8 * np.linalg.norm(_np(b))
+
+
+# ---------------------------------------------------------------- what the documents allow
+@pytest.mark.parametrize("kind", ["bf16", "w4"])
+@pytest.mark.parametrize("T", [3, 40])
+def test_rows_off_alignment_an_output_given_and_what_is_around_it(T, kind):
+    rng = np.random.default_rng(T)
+    E, k, H, I = 2, 2, 264, 136
+    up, down, *_ = _experts(rng, E, H, I, kind)
+    x = _bf16(rng.integers(-2, 3, (T, H)))
+    ids, w = (_cuda(a) for a in _choices(rng, T, E, k))
+    want = tg.moe_mlp(x, ids, w, up, down)
+    store = torch.full(((T + 2) * H + 1,), 7.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.empty(T * H + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H)
+    off.copy_(x)
+    out = store[H + 1:(T + 1) * H + 1].view(T, H)
+    got = tg.moe_mlp(off, ids, w, up, down, out=out)
+    assert got is out and bool((store[:H + 1] == 7.0).all()) and bool((store[(T + 1) * H + 1:] == 7.0).all())
+    # the same sums in the same order (one block of either reduction)
+    assert torch.equal(out, want)
+    logits = torch.randn((T, E), device="cuda")
+    y, i, s = tg.moe_layer(off, logits, up, down, k, out=out)
+    assert y is out and torch.equal(y, tg.moe_mlp(x, i, s, up, down))
+
+
+def test_a_layer_with_masked_rows():
+    rng = np.random.default_rng(2)
+    up, down, *_ = _experts(rng, 6, 64, 48, "w4")
+    x = torch.randn((5, 64), device="cuda").to(torch.bfloat16)
+    logits = torch.randn((5, 6), device="cuda")
+    clean, *_ = tg.moe_layer(x, logits, up, down, 2)
+    logits[1] = -float("inf")                          # nothing is left
+    logits[3] = torch.finfo(torch.float32).min         # all alike
+    logits[4, 2] = float("nan")
+    y, ids, w = tg.moe_layer(x, logits, up, down, 2)
+    assert not bool(y[1].any()) and ids[1].tolist() == [0, 1] and w[1].tolist() == [0.0, 0.0]
+    assert ids[3].tolist() == [0, 1] and w[3].tolist() == [0.5, 0.5] and bool(torch.isfinite(y[3]).all())
+    assert ids[4].tolist()[0] == 2 and bool(torch.isnan(y[4]).all())
+    assert torch.equal(y[[0, 2]], clean[[0, 2]])
+
+
+@pytest.mark.parametrize("T,E,k,H,I,kind", [(64, 1024, 16, 16, 16, "bf16"), (2, 1, 1, 65536, 16, "bf16"),
+                                            (20, 1, 1, 65536, 16, "w4"), (2, 1, 1, 16, 65536, "w4"),
+                                            (20, 1, 1, 16, 65536, "bf16")])
+def test_experts_at_their_limits(T, E, k, H, I, kind):
+    rng = np.random.default_rng(H + I)
+    up, down, g, u, d = _experts(rng, E, H, I, kind, 128, False)
+    x = np.zeros((T, H))
+    x[:, rng.choice(H, 64, replace=H < 64)] = rng.integers(-2, 3, (T, 64))
+    x[:, -1] = 1.0
+    ids, w = _choices(rng, T, E, k)
+    mark(f"experts at their limits T{T} E{E} k{k} H{H} I{I} {kind}")
+    y = tg.moe_mlp(_bf16(x), _cuda(ids), _cuda(w), up, down)
+    torch.cuda.synchronize()
+    # up to 32 blocks of two chunks one after the other: 4 + 32 more additions than _check_close counts, as 32 of its 48
+    # are the k pairs and waves of larger layers
+    _check_close(y, x, ids, w, g, u, d, "silu")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 16, 2 ** 21), (70, 16, 2 ** 21), (3, 2 ** 21, 32), (2 ** 20, 16, 40)])
+def test_gemm_w4_at_its_limits(M, N, K):
+    rng = np.random.default_rng(M + N)
+    P, C, G = -(-N // 16), -(-K // 128), -(-K // 128)
+    words = torch.randint(-2 ** 31, 2 ** 31, (P, C, 64, 4), dtype=torch.int32, device="cuda")
+    q = tg.W4(words, torch.ones((P, G, 16), device="cuda"), None, K, N, 128)
+    # at most 32 of a row's elements are not zero: integers, exact
+    at = np.unique(np.concatenate([rng.choice(K, 30), [0, K - 1]]))
+    A = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    some = torch.from_numpy(rng.integers(-4, 5, (M, len(at))).astype(np.float32)).cuda()
+    cols = torch.from_numpy(at).cuda()
+    A[:, cols] = some.to(torch.bfloat16)
+    mark(f"gemm_w4 at its limits {M}x{N}x{K}")
+    C_ = tg.gemm_w4(A, q, out_dtype=torch.float32)
+    n = torch.arange(N, device="cuda")
+    ref = torch.zeros((M, N), device="cuda")
+    for i, k in enumerate(at.tolist()):
+        word = words[n // 16, k // 128, 16 * (k % 32 // 8) + n % 16, k % 128 // 32]
+        code = (word >> (4 * (k % 8 // 2 + 4 * (k % 2)))) & 15
+        ref += some[:, i:i + 1] * (code.float() - 8.0)
+    assert torch.equal(C_, ref)
+
+
+def test_route_and_quantize_at_their_limits():
+    T = 2 ** 24
+    logits = torch.randn((T, 2), device="cuda").to(torch.bfloat16)
+    ids, w = tg.moe_route(logits, 1, renorm=True)
+    assert torch.equal(ids[:, 0], (logits[:, 1] > logits[:, 0]).to(torch.int32)) and bool((w == 1.0).all())
+    for K, N in ((2 ** 21, 3), (3, 2 ** 21)):
+        W = (torch.randint(-7, 8, (K, N), device="cuda")).float()
+        W[::32] = 7.0                                  # every group's scale is 1: the codes hold W
+        q, v = tg.w4_quantize(W, 32, values=True)
+        assert torch.equal(v, W) and bool((q.scales[:, :, :3] == 1.0).all())

@@ -14,7 +14,7 @@
 // the others go on in the other half of the buffer.  For 16 rows of 28672 x
 // 8192 in 4 bits: loads of a panel for every wave's own A 79 us, rows kept and
 // panels streamed 42, scales left as loaded until their step 30, a barrier for
-// four panels and the next block's words ahead 27 on that day's card, 31 on
+// four panels and the next block's words ahead 27 on one card, 31 on
 // others (with zero points 31 to 34, 3.6 to 4.0 TB/s).  What is left over the 24
 // us of a copy is the start of the stream, the meeting of the sums and 36 VALU
 // instructions a KiB of codes.
