@@ -522,6 +522,117 @@ int tg_moe_layer(int64_t T, int64_t H, int64_t I, int64_t E, int k, const void *
                  int logits_dtype, int renorm, const tg_weight *gate_up, const tg_weight *down, void *y, int32_t *ids,
                  float *weights, int gate, void *workspace, size_t workspace_bytes);
 
+/* ---------------------------------------------------------------- 8-bit matrices */
+/*
+ * A matrix of R rows x K columns (K: the index that products sum over) in
+ * e4m3 (4 exponent bits, 3 mantissa bits, no infinity, largest value 448) with
+ * fp32 scales.  codes: bytes [R][Kp], Kp = 128 ceil(K / 128), 16-byte aligned,
+ * zero past K.  block: 1, 128 elements of a row share a scale, scales are
+ * [R][Kp / 128]; or 128, blocks of 128 x 128 do, scales are [ceil(R / 128)][Kp / 128].
+ * An element is code * scale.  A stack of matrices is stored one after the
+ * other, codes and scales each.
+ */
+typedef struct {
+    const void *codes;
+    const float *scales;
+    int32_t block, reserved;
+} tg_f8;
+
+/*
+ * Quantises `count` R x K matrices.  x: fp32 or bf16 (dtype = TG_F32 or
+ * TG_BF16), each matrix [R][K] if rows_first, else [K][R] (the transpose is
+ * quantised); codes, scales and block as above; values (may be NULL): what the
+ * codes stand for, in x's order and type.
+ *   scale = fp32(max |x| / 448) over the block
+ *   code  = the e4m3 nearest to x / scale (exact quotient, ties to even,
+ *           at most 448); 0 where scale is 0
+ *   value = code * scale, rounded to fp32, then to x's type
+ * A block that holds an infinity or NaN has NaN as its scale, codes and values.
+ * Elements of x have element alignment, codes 16 bytes; the outputs must not
+ * overlap x.  Asynchronous on the stream of tg_set_stream, as are all
+ * functions of this and the next section; none of them allocates, so each may
+ * be captured into a graph.  Bad arguments are TG_E_INVAL, before anything is
+ * queued.  Limits: R, K <= 2^24, count <= 65535, a matrix of fewer than 2^40
+ * elements (TG_E_UNSUPPORTED).
+ */
+int tg_fp8_quantize(int64_t count, int64_t R, int64_t K, int block, const void *x, int dtype, int rows_first,
+                    void *codes, float *scales, void *values);
+
+/*
+ * C = act(A . B^T + bias): A M x K with block 1, B N x K (a layer's output rows
+ * x input columns) with block 1 or 128; C M x N bf16 or fp32 (dtype = TG_BF16
+ * or TG_BF16_F32OUT), row-major, element alignment; bias N floats or NULL; act a
+ * tg_act.  With activations as A and weights as B this is a layer; with output
+ * gradients and the transposed weights it is the input's gradient, with the
+ * transposes of output gradients and of activations (both block 1) the weights'.
+ * Products of codes are summed in fp32, 128 k at a time, and those sums times
+ * the fp32 product of their two scales are added up in fp32: scales whose
+ * product is below 2^-126 lose bits, above 2^128 they give infinities.  Rows
+ * and columns with NaN codes or scales give NaN in their own results only.
+ * workspace: device memory of tg_gemm_fp8_workspace_bytes(M, N, K), 16-byte
+ * aligned (NULL where that is 0), not shared by calls that may overlap.  C must
+ * not overlap the inputs.  The same call gives the same bits.
+ * Limits: M, N, K <= 2^24 (TG_E_UNSUPPORTED).
+ */
+int tg_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
+int tg_gemm_fp8(int64_t M, int64_t N, int64_t K, const tg_f8 *A, const tg_f8 *B, const float *bias, void *C,
+                int dtype, int act, void *workspace, size_t workspace_bytes);
+
+/* ---------------------------------------------------------------- experts on many tokens */
+/*
+ * The (token, choice) pairs sorted by expert.  ids: int32 T x k, as tg_moe_route
+ * gives them.  Pair t k + j of expert e = ids[t][j] gets row position[t][j];
+ * expert e has the rows offsets[e] .. offsets[e + 1] - 1, in the order of their
+ * pairs; source[row] is the row's pair.  Pairs whose id is outside [0, E) (padding,
+ * experts kept elsewhere) have position -1 and no row; source is -1 for the rows from
+ * offsets[E] on.  position: T x k, source: T k, offsets: E + 1, all int32.
+ * workspace: device memory of tg_moe_sort_workspace_bytes(T, E, k), 16-byte
+ * aligned (NULL where that is 0), not shared by calls that may overlap.
+ * Limits: E <= 1024, k <= 16, T <= 2^24 (TG_E_UNSUPPORTED).
+ */
+int tg_moe_sort_workspace_bytes(int64_t T, int64_t E, int k, size_t *bytes);
+int tg_moe_sort(int64_t T, int64_t E, int k, const int32_t *ids, int32_t *position, int32_t *source,
+                int32_t *offsets, void *workspace, size_t workspace_bytes);
+
+/*
+ * Brings tokens into the order of the experts: out[position[t][j]] = x[t], rows
+ * of row_bytes bytes; and out2 = x2 with rows of row2_bytes in the same way, if
+ * row2_bytes is not 0 (the scales of 8-bit rows).  Positions outside [0, rows)
+ * are skipped, and rows that no pair has are left as they were.  Any alignment; no
+ * overlap.  The gradient of x is tg_moe_combine of out's without weights.
+ * Limits: k <= 16, T <= 2^24, rows < 2^31, row bytes <= 2^24 (TG_E_UNSUPPORTED).
+ */
+int tg_moe_gather(int64_t T, int k, int64_t rows, const int32_t *position, int64_t row_bytes, const void *x,
+                  void *out, int64_t row2_bytes, const void *x2, void *out2);
+
+/*
+ * tg_gemm_fp8 for each expert on its own rows: C[r] = A[r] . B_e^T for the rows r
+ * in offsets[e] .. offsets[e + 1] - 1.  A: `rows` x K, block 1; B: a stack of E
+ * matrices N x K; C: rows x N, bf16 or fp32.  offsets: E + 1 int32 on the device,
+ * rising; what they name outside [0, rows) is skipped.  Rows outside every
+ * expert's are not read, and left as they were in C.
+ * Limits: E <= 1024, rows, N, K <= 2^24 (TG_E_UNSUPPORTED).
+ */
+int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8 *A, const tg_f8 *B,
+                    const int32_t *offsets, void *C, int dtype);
+
+/*
+ * y[t] = sum_j weights[t][j] * x[position[t][j]], j in order, fp32 sums, rounded
+ * once; weights fp32 T x k, or NULL: all 1.  x: rows x H, y: T x H, both fp32 or bf16
+ * (dtype = TG_F32 or TG_BF16).  Positions outside [0, rows) add nothing; a token
+ * without any gets zeros.
+ * tg_moe_combine_grad: its gradients, dy T x H and x given,
+ *   dx[position[t][j]] = weights[t][j] * dy[t]     (x's type; other rows as they were)
+ *   dweights[t][j]     = sum_h dy[t][h] * x[position[t][j]][h]   (fp32; 0 without a row)
+ * The same call gives the same bits.  Element alignment; outputs must not
+ * overlap inputs.  Limits: k <= 16, T <= 2^24, H <= 2^24, rows < 2^31
+ * (TG_E_UNSUPPORTED).
+ */
+int tg_moe_combine(int64_t T, int k, int64_t rows, int64_t H, const void *x, int dtype, const int32_t *position,
+                   const float *weights, void *y);
+int tg_moe_combine_grad(int64_t T, int k, int64_t rows, int64_t H, const void *dy, const void *x, int dtype,
+                        const int32_t *position, const float *weights, void *dx, float *dweights);
+
 #ifdef __cplusplus
 }
 #endif

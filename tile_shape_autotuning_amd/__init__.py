@@ -18,6 +18,8 @@ from ._native import (ACT, BF16, BF16_F32OUT, F32, Cfg, DeviceDesc, TileGemmErro
                       set_tile_order, tile_order,
                       rmsnorm_cache_lookup, rmsnorm_tunes)
 from .experts import W4, gemm_w4, moe_layer, moe_mlp, moe_route, w4_quantize
+from .fp8 import F8, fp8_quantize, gemm_fp8, moe_gemm_fp8
+from .order import MoeOrder, moe_combine, moe_combine_grad, moe_gather, moe_sort
 
 __all__ = [
     "gemm_bias_act", "gemm_autotune", "Cfg", "DeviceDesc", "TileGemmError", "F32", "BF16", "BF16_F32OUT",
@@ -28,6 +30,8 @@ __all__ = [
     "tile_order",
     "rmsnorm", "rmsnorm_autotune", "rmsnorm_cache_lookup", "rmsnorm_tunes",
     "W4", "w4_quantize", "gemm_w4", "moe_route", "moe_mlp", "moe_layer",
+    "F8", "fp8_quantize", "gemm_fp8", "moe_gemm_fp8",
+    "MoeOrder", "moe_sort", "moe_gather", "moe_combine", "moe_combine_grad",
 ]
 
 

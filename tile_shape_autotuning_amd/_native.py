@@ -32,6 +32,8 @@ EXPORTS = [
     "tg_cache_size", "tg_stats", "tg_set_shape_buckets", "tg_dispatch_m", "tg_set_tile_order", "tg_tile_order",
     "tg_rmsnorm", "tg_rmsnorm_autotune", "tg_rmsnorm_cache_lookup", "tg_rmsnorm_tunes",
     "tg_w4_quantize", "tg_gemm_w4", "tg_moe_route", "tg_moe_workspace_bytes", "tg_moe_mlp", "tg_moe_layer",
+    "tg_fp8_quantize", "tg_gemm_fp8_workspace_bytes", "tg_gemm_fp8", "tg_moe_sort_workspace_bytes", "tg_moe_sort",
+    "tg_moe_gather", "tg_moe_gemm_fp8", "tg_moe_combine", "tg_moe_combine_grad",
 ]
 
 
@@ -82,6 +84,12 @@ class Weight(ctypes.Structure):
                 ("zeros", ctypes.c_void_p)]
 
 
+class F8Matrix(ctypes.Structure):
+    """tg_f8: a stack of 8-bit matrices on the device."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("block", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class TileGemmError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
@@ -101,6 +109,7 @@ def lib():
         i64, i32, vp, dp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.POINTER(ctypes.c_double)
         pc = ctypes.POINTER(Cfg)
         pw = ctypes.POINTER(Weight)
+        p8 = ctypes.POINTER(F8Matrix)
         pi = ctypes.POINTER(ctypes.c_int)
         pi64 = ctypes.POINTER(ctypes.c_int64)
         sig = {
@@ -150,6 +159,15 @@ def lib():
             "tg_moe_mlp": ([i64, i64, i64, i64, i32, vp, vp, vp, pw, pw, vp, i32, vp, ctypes.c_size_t], i32),
             "tg_moe_layer": ([i64, i64, i64, i64, i32, vp, vp, i32, i32, pw, pw, vp, vp, vp, i32, vp,
                               ctypes.c_size_t], i32),
+            "tg_fp8_quantize": ([i64, i64, i64, i32, vp, i32, i32, vp, vp, vp], i32),
+            "tg_gemm_fp8_workspace_bytes": ([i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)], i32),
+            "tg_gemm_fp8": ([i64, i64, i64, p8, p8, vp, vp, i32, i32, vp, ctypes.c_size_t], i32),
+            "tg_moe_sort_workspace_bytes": ([i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)], i32),
+            "tg_moe_sort": ([i64, i64, i32, vp, vp, vp, vp, vp, ctypes.c_size_t], i32),
+            "tg_moe_gather": ([i64, i32, i64, vp, i64, vp, vp, i64, vp, vp], i32),
+            "tg_moe_gemm_fp8": ([i64, i64, i64, i64, p8, p8, vp, vp, i32], i32),
+            "tg_moe_combine": ([i64, i32, i64, i64, vp, i32, vp, vp, vp], i32),
+            "tg_moe_combine_grad": ([i64, i32, i64, i64, vp, vp, i32, vp, vp, vp, vp], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -421,6 +439,47 @@ def moe_layer_ptr(T, H, I, E, k, x, logits, logits_dtype, renorm, gate_up, down,
                   workspace_bytes) -> int:
     return lib().tg_moe_layer(T, H, I, E, k, x, logits, logits_dtype, 1 if renorm else 0, gate_up, down, y, ids,
                               weights, gate, workspace, workspace_bytes)
+
+
+# ---------------------------------------------------------------- 8-bit matrices and sorted experts (device addresses)
+def fp8_quantize_ptr(count, R, K, block, x, dtype, rows_first, codes, scales, values) -> int:
+    return lib().tg_fp8_quantize(count, R, K, block, x, dtype, 1 if rows_first else 0, codes, scales, values)
+
+
+def gemm_fp8_workspace_bytes(M, N, K) -> int:
+    n = ctypes.c_size_t()
+    check(lib().tg_gemm_fp8_workspace_bytes(M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def gemm_fp8_ptr(M, N, K, A, B, bias, C, dtype, act, workspace, workspace_bytes) -> int:
+    return lib().tg_gemm_fp8(M, N, K, A, B, bias, C, dtype, act, workspace, workspace_bytes)
+
+
+def moe_sort_workspace_bytes(T, E, k) -> int:
+    n = ctypes.c_size_t()
+    check(lib().tg_moe_sort_workspace_bytes(T, E, k, ctypes.byref(n)))
+    return n.value
+
+
+def moe_sort_ptr(T, E, k, ids, position, source, offsets, workspace, workspace_bytes) -> int:
+    return lib().tg_moe_sort(T, E, k, ids, position, source, offsets, workspace, workspace_bytes)
+
+
+def moe_gather_ptr(T, k, rows, position, row_bytes, x, out, row2_bytes, x2, out2) -> int:
+    return lib().tg_moe_gather(T, k, rows, position, row_bytes, x, out, row2_bytes, x2, out2)
+
+
+def moe_gemm_fp8_ptr(rows, E, N, K, A, B, offsets, C, dtype) -> int:
+    return lib().tg_moe_gemm_fp8(rows, E, N, K, A, B, offsets, C, dtype)
+
+
+def moe_combine_ptr(T, k, rows, H, x, dtype, position, weights, y) -> int:
+    return lib().tg_moe_combine(T, k, rows, H, x, dtype, position, weights, y)
+
+
+def moe_combine_grad_ptr(T, k, rows, H, dy, x, dtype, position, weights, dx, dweights) -> int:
+    return lib().tg_moe_combine_grad(T, k, rows, H, dy, x, dtype, position, weights, dx, dweights)
 
 
 def stats():
