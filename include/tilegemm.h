@@ -565,14 +565,19 @@ int tg_fp8_quantize(int64_t count, int64_t R, int64_t K, int block, const void *
  * tg_act.  With activations as A and weights as B this is a layer; with output
  * gradients and the transposed weights it is the input's gradient, with the
  * transposes of output gradients and of activations (both block 1) the weights'.
- * Products of codes are summed in fp32, 128 k at a time, and those sums times
- * the fp32 product of their two scales are added up in fp32: scales whose
- * product is below 2^-126 lose bits, above 2^128 they give infinities.  Rows
- * and columns with NaN codes or scales give NaN in their own results only.
+ * Products of codes are summed 128 k at a time, and those sums times the fp32
+ * product of their two scales are added up in fp32: scales whose product is
+ * below 2^-126 lose bits, above 2^128 they give infinities.  An fp32 C has all
+ * its sums in fp32.  A bf16 C may have the sums of a chunk from the 8-bit form of
+ * the matrix cores, which cuts each eight products to multiples of 2^-13 of
+ * (the power of two of) the largest before it adds them in fp32: results are off
+ * by 2e-5 of their size in the mean, at most by 7/8192 of the largest of each
+ * eight products, where the rounding to bf16 is off by up to 4e-3.  Rows and
+ * columns with NaN codes or scales give NaN in their own results only.
  * workspace: device memory of tg_gemm_fp8_workspace_bytes(M, N, K), 16-byte
  * aligned (NULL where that is 0), not shared by calls that may overlap.  C must
  * not overlap the inputs.  The same call gives the same bits.
- * Limits: M, N, K <= 2^24 (TG_E_UNSUPPORTED).
+ * Limits: M, N <= 2^24, K <= 2^22 (TG_E_UNSUPPORTED).
  */
 int tg_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
 int tg_gemm_fp8(int64_t M, int64_t N, int64_t K, const tg_f8 *A, const tg_f8 *B, const float *bias, void *C,
@@ -611,7 +616,7 @@ int tg_moe_gather(int64_t T, int k, int64_t rows, const int32_t *position, int64
  * matrices N x K; C: rows x N, bf16 or fp32.  offsets: E + 1 int32 on the device,
  * rising; what they name outside [0, rows) is skipped.  Rows outside every
  * expert's are not read, and left as they were in C.
- * Limits: E <= 1024, rows, N, K <= 2^24 (TG_E_UNSUPPORTED).
+ * Limits: E <= 1024, rows, N <= 2^24, K <= 2^22 (TG_E_UNSUPPORTED).
  */
 int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8 *A, const tg_f8 *B,
                     const int32_t *offsets, void *C, int dtype);

@@ -142,9 +142,9 @@ def test_expert_products_refuse(kw):
 
 
 def test_product_limits_and_empty():
-    for kw in (dict(M=BIG), dict(N=BIG), dict(K=BIG)):
+    for kw in (dict(M=BIG), dict(N=BIG), dict(K=(1 << 22) + 1)):
         assert _gemm(**kw) == N.TG_E_UNSUPPORTED
-    for kw in (dict(rows=BIG), dict(N=BIG), dict(K=BIG), dict(E=1025)):
+    for kw in (dict(rows=BIG), dict(N=BIG), dict(K=(1 << 22) + 1), dict(E=1025)):
         assert _experts(**kw) == N.TG_E_UNSUPPORTED
     assert _gemm(M=0, A=None, C=None) == N.TG_OK and _gemm(N=0, B=None) == N.TG_OK
     assert _experts(rows=0, A=None, C=None) == N.TG_OK and _experts(N=0, B=None) == N.TG_OK

@@ -5,7 +5,9 @@
 //
 // A chunk of 128 k of 16 x 16 results is summed from zero; a lane's four sums are
 // multiplied by their scales as they are added up, in fp32.  B is the first
-// operand: a lane then has one row m and four neighbouring columns n.
+// operand: a lane then has one row m and four neighbouring columns n.  fp32
+// results take the exact form of the products, bf16 results of many rows the
+// fast one (fp8.hpp).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -15,6 +17,8 @@
 #include "fp8_host.hpp"
 
 namespace tg {
+
+constexpr int64_t kMaxDepth = (int64_t)1 << 22;        // 256 rows of A or B stay within 32-bit offsets
 
 struct F8Params {
     const unsigned char *A, *B;
@@ -26,7 +30,34 @@ struct F8Params {
     int chunks, E;
     int b_rows;                                        // rows of B that share a scale, 1 or 128
     int out_bf16, act;
+    int vec_out;                                       // four results of a row are one aligned access
+    int group_m;                                       // row tiles that go through the column tiles together
 };
+
+// How many tiles of BM rows the experts up to `e` of its group of 64 have (lane
+// by lane), and the rows [lo, hi) of expert e.
+template <int BM>
+__device__ __forceinline__ int expert_tiles(const F8Params& p, int e, int lane, int64_t& lo, int64_t& hi)
+{
+    lo = hi = 0;
+    if (e < p.E) {
+        lo = max((int64_t)0, (int64_t)p.offsets[e]);
+        hi = min(p.M, (int64_t)p.offsets[e + 1]);
+    }
+    int n = hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(n, off);
+        n += lane >= off ? o : 0;
+    }
+    return n;
+}
+
+}  // namespace tg
+
+#include "gemm_fp8_tiles.hpp"
+
+namespace tg {
 
 // The rows [begin, end) and the matrix of B that row tile `tile` of BM rows
 // belongs to; false past the last tile.
@@ -100,8 +131,27 @@ __global__ void __launch_bounds__(256) gemm_fp8_kernel(F8Params p)
     }
 }
 
-static int launch_gemm(const F8Params& p, hipStream_t s)
+template <int BM, int BN, int WGM, int WGN, bool BROWS, bool EXACT>
+static int launch_tiles(const F8Params& p, hipStream_t s)
 {
+    using Cf = F8Tile<BM, BN, WGM, WGN, BROWS>;
+    const int64_t tiles_m = ceil_div(p.M, BM) + (p.offsets ? std::min<int64_t>(p.E, p.M) : 0);
+    hipLaunchKernelGGL((gemm_fp8_tiles_kernel<BM, BN, WGM, WGN, BROWS, EXACT>),
+                       dim3((unsigned)(tiles_m * ceil_div(p.N, BN))), dim3(Cf::T), Cf::LDS, s, p);
+    return launched("gemm_fp8 launch");
+}
+
+static int launch_gemm(F8Params p, hipStream_t s)
+{
+    p.group_m = 8;
+    p.vec_out = p.N % 4 == 0 && (uintptr_t)p.C % (p.out_bf16 ? 8 : 16) == 0;
+    if (p.M > 64) {
+        if (p.out_bf16)
+            return p.b_rows == 1 ? launch_tiles<256, 256, 2, 4, true, false>(p, s)
+                                 : launch_tiles<256, 256, 2, 4, false, false>(p, s);
+        return p.b_rows == 1 ? launch_tiles<128, 128, 2, 2, true, true>(p, s)
+                             : launch_tiles<128, 128, 2, 2, false, true>(p, s);
+    }
     const int64_t tiles = ceil_div(p.M, 16) + (p.offsets ? p.E : 0);
     hipLaunchKernelGGL(gemm_fp8_kernel, dim3((unsigned)tiles, (unsigned)std::min<int64_t>(ceil_div(p.N, 256), 65535)),
                        dim3(256), 0, s, p);
@@ -114,8 +164,8 @@ static int check_product(int64_t M, int64_t N, int64_t K, int dtype)
         return set_error(TG_E_INVAL, "rows and N must be >= 0, K >= 1");
     if (dtype != TG_BF16 && dtype != TG_BF16_F32OUT)
         return set_error(TG_E_INVAL, "C is bf16 (TG_BF16) or fp32 (TG_BF16_F32OUT)");
-    if (M > kMaxSide || N > kMaxSide || K > kMaxSide)
-        return set_error(TG_E_UNSUPPORTED, "rows, N and K are at most 2^24");
+    if (M > kMaxSide || N > kMaxSide || K > kMaxDepth)
+        return set_error(TG_E_UNSUPPORTED, "rows and N are at most 2^24, K 2^22");
     return TG_OK;
 }
 
@@ -150,7 +200,7 @@ extern "C" {
 
 int tg_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes)
 {
-    if (!bytes || M < 0 || N < 0 || K < 1 || M > kMaxSide || N > kMaxSide || K > kMaxSide)
+    if (!bytes || M < 0 || N < 0 || K < 1 || M > kMaxSide || N > kMaxSide || K > kMaxDepth)
         return set_error(TG_E_INVAL, "bad size, or bytes is NULL");
     *bytes = 0;
     return TG_OK;

@@ -111,8 +111,9 @@ def gemm_fp8(A, B, bias=None, act="none", out=None, out_dtype=None):
 
     A: an F8 of M x K, block 1; B: an F8 of N x K (a layer's output rows x input
     columns), block 1 or 128; bias: [N] float32 or None; act: "none" | "relu" |
-    "gelu"; out_dtype: torch.bfloat16 (default) or torch.float32.  Runs on the
-    current stream and returns C [M, N].
+    "gelu"; out_dtype: torch.bfloat16 (default) or torch.float32, which also has
+    the more exact sums (tilegemm.h).  Runs on the current stream and returns C
+    [M, N].
 
     A layer and its gradients, x [T, K], W [N, K], dy [T, N]:
       y  = gemm_fp8(fp8_quantize(x), fp8_quantize(W, 128))
