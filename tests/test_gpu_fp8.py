@@ -315,7 +315,8 @@ def _ids(rng, T, E, k, kind):
 ORDERS = [(1, 8, 2, "plain"), (1, 1, 1, "plain"), (5, 16, 4, "away"), (64, 64, 6, "plain"), (257, 8, 3, "repeats"),
           (1000, 256, 8, "away"), (3, 1024, 16, "plain"), (4099, 64, 8, "plain"), (2500, 1024, 5, "away"),
           (3000, 7, 7, "plain"), (700, 5, 2, "one"), (50, 4, 2, "none"), (40000, 33, 3, "repeats"), (2048, 128, 1, "plain"),
-          (20000, 2, 16, "one")]
+          (20000, 2, 16, "one"), (256, 16, 8, "plain"), (257, 16, 8, "away"), (50000, 1024, 16, "plain"), (3000, 1, 1, "one"),
+          (70000, 300, 4, "repeats"), (1025, 3, 2, "none")]
 
 
 @pytest.mark.parametrize("T,E,k,kind", ORDERS)
@@ -339,7 +340,7 @@ def test_sort_of_nothing():
 
 ROWS = [(1, 8, 2, 16, "plain"), (5, 16, 4, 1000, "away"), (33, 4, 2, 1, "plain"), (70, 8, 8, 259, "away"),
         (300, 64, 6, 2048, "plain"), (9, 16, 16, 8192, "plain"), (40, 3, 2, 77, "repeats"), (20, 4, 3, 30, "none"),
-        (130, 32, 5, 514, "away")]
+        (130, 32, 5, 514, "away"), (6, 4, 2, 2052, "plain"), (6, 8, 5, 4104, "away"), (3, 4, 3, 5, "plain")]
 
 
 def _order(ids, E):

@@ -167,6 +167,11 @@ def test_sort_refuses(kw):
 
 
 def test_sort_limits():
+    # many pairs: counts of blocks of experts, in the workspace
+    need = N.moe_sort_workspace_bytes(4096, 64, 8)
+    assert need > 0 and N.moe_sort_workspace_bytes(16, 64, 8) == 0 and N.moe_sort_workspace_bytes(0, 1, 1) == 0
+    for kw in (dict(ws=None), dict(ws=BUF + 8), dict(ws_bytes=need - 1)):
+        assert _sort(T=4096, E=64, k=8, **kw) == N.TG_E_INVAL
     for kw in (dict(T=BIG), dict(E=1025), dict(k=17)):
         assert _sort(**kw) == N.TG_E_UNSUPPORTED
     n = ctypes.c_size_t()

@@ -13,35 +13,32 @@
 namespace tg {
 
 constexpr int kOrderExperts = 1024, kOrderChoices = 16;
+constexpr int64_t kUnits = (int64_t)1 << 31;           // pieces of all rows of a call
 constexpr int64_t kOrderTokens = (int64_t)1 << 24, kOrderWidth = (int64_t)1 << 24;
 
 // ---------------------------------------------------------------- sort
-// A workgroup takes one expert: it counts the pairs of the experts before it,
-// then walks the pairs in order and numbers its own.  The last workgroup takes
-// the pairs without an expert, and the rows behind the last one.
-__global__ void __launch_bounds__(256) moe_sort_kernel(const int32_t* ids, int64_t n, int E, int32_t* position,
-                                                       int32_t* source, int32_t* offsets)
+// Few pairs: a workgroup takes one expert, counts the pairs of the experts before
+// it, then walks the pairs in order and numbers its own.  The last workgroup
+// takes the pairs without an expert, and the rows behind the last one.
+__global__ void __launch_bounds__(256) moe_sort_few_kernel(const int32_t* ids, int n, int E, int32_t* position,
+                                                           int32_t* source, int32_t* offsets)
 {
     __shared__ int part[4];
     const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    auto total = [&](int v) {                          // over the workgroup
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            v += __shfl_xor(v, off);
-        __syncthreads();
-        if (lane == 0)
-            part[wave] = v;
-        __syncthreads();
-        return part[0] + part[1] + part[2] + part[3];
-    };
     int before = 0;
-    for (int64_t i = threadIdx.x; i < n; i += 256)
+    for (int i = threadIdx.x; i < n; i += 256)
         before += ids[i] >= 0 && ids[i] < e;
-    int at = total(before);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        before += __shfl_xor(before, off);
+    if (lane == 0)
+        part[wave] = before;
+    __syncthreads();
+    int at = part[0] + part[1] + part[2] + part[3];
     if (threadIdx.x == 0)
         offsets[e] = at;
     if (e == E) {
-        for (int64_t i = threadIdx.x; i < n; i += 256) {
+        for (int i = threadIdx.x; i < n; i += 256) {
             if (ids[i] < 0 || ids[i] >= E)
                 position[i] = -1;
             if (i >= at)
@@ -49,8 +46,8 @@ __global__ void __launch_bounds__(256) moe_sort_kernel(const int32_t* ids, int64
         }
         return;
     }
-    for (int64_t i0 = 0; i0 < n; i0 += 256) {
-        const int64_t i = i0 + threadIdx.x;
+    for (int i0 = 0; i0 < n; i0 += 256) {
+        const int i = i0 + threadIdx.x;
         const bool mine = i < n && ids[i] == e;
         const unsigned long long has = __ballot(mine);
         __syncthreads();
@@ -62,51 +59,201 @@ __global__ void __launch_bounds__(256) moe_sort_kernel(const int32_t* ids, int64
             to += part[w];
         if (mine) {
             position[i] = to;
-            source[to] = (int32_t)i;
+            source[to] = i;
         }
         at += part[0] + part[1] + part[2] + part[3];
     }
+}
+
+// Many pairs: blocks of `per` pairs are counted by expert, then every block adds
+// up the counts of all blocks (for the experts' first rows) and of those before
+// it, and numbers its own pairs, 64 of a wave at a time.
+struct SortParams {
+    const int32_t* ids;
+    int32_t *position, *source, *offsets, *counts;     // counts: [blocks][E]
+    int n, E, per, blocks;
+};
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+
+__global__ void __launch_bounds__(kSortThreads) moe_count_kernel(SortParams p)
+{
+    __shared__ int count[kOrderExperts];
+    for (int e = threadIdx.x; e < p.E; e += kSortThreads)
+        count[e] = 0;
+    __syncthreads();
+    const int first = blockIdx.x * p.per, last = min(p.n, first + p.per);
+    for (int i = first + threadIdx.x; i < last; i += kSortThreads) {
+        const int e = p.ids[i];
+        if ((unsigned)e < (unsigned)p.E)
+            atomicAdd(&count[e], 1);                   // sums of ones: any order
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kSortThreads)
+        p.counts[blockIdx.x * p.E + e] = count[e];
+}
+
+__global__ void __launch_bounds__(kSortThreads) moe_place_kernel(SortParams p)
+{
+    extern __shared__ int next[];                      // [waves][E]: the row of a wave's next pair of an expert
+    __shared__ int sums[2][kSortThreads];              // all pairs of an expert, and those of the blocks before
+    __shared__ int part[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int first = blockIdx.x * p.per, last = min(p.n, first + p.per);
+    const int each = p.per / kSortWaves, from = first + wave * each, to = min(last, from + each);
+    for (int i = tid; i < kSortWaves * p.E; i += kSortThreads)
+        next[i] = 0;
+    sums[0][tid] = sums[1][tid] = 0;
+    __syncthreads();
+    for (int i = from + lane; i < to; i += 64) {
+        const int e = p.ids[i];
+        if ((unsigned)e < (unsigned)p.E)
+            atomicAdd(&next[wave * p.E + e], 1);
+    }
+    // several threads an expert, where there are fewer experts than threads, take blocks in turn
+    const int turns = kSortThreads / p.E;
+    if (tid < turns * p.E) {
+        const int e = tid % p.E;
+        int all = 0, before = 0;
+#pragma unroll 8
+        for (int b = tid / p.E; b < p.blocks; b += turns) {
+            const int c = p.counts[b * p.E + e];
+            all += c;
+            before += b < (int)blockIdx.x ? c : 0;
+        }
+        atomicAdd(&sums[0][e], all);
+        atomicAdd(&sums[1][e], before);
+    }
+    __syncthreads();
+    // rows before this expert's: a sum over the experts before it
+    const int all = sums[0][tid];
+    int upto = all;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(upto, off);
+        upto += lane >= off ? o : 0;
+    }
+    if (lane == 63)
+        part[wave] = upto;
+    __syncthreads();
+    int rows = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+        upto += w < wave ? part[w] : 0;
+        rows += part[w];
+    }
+    if (tid < p.E) {
+        if (blockIdx.x == 0)
+            p.offsets[tid] = upto - all;
+        int at = upto - all + sums[1][tid];
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = next[w * p.E + tid];
+            next[w * p.E + tid] = at;
+            at += c;
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0)
+        p.offsets[p.E] = rows;
+    for (int i = max(first, rows) + tid; i < last; i += kSortThreads)
+        p.source[i] = -1;
+    __syncthreads();
+    for (int i0 = from; i0 < to; i0 += 64) {
+        const int i = i0 + lane;
+        const int e = i < to ? p.ids[i] : -1;
+        const bool has = (unsigned)e < (unsigned)p.E;
+        // lanes with the same expert
+        unsigned long long same = __ballot(has);
+        for (int bit = 1; bit < p.E; bit <<= 1) {
+            const unsigned long long set = __ballot(has && (e & bit));
+            same &= e & bit ? set : ~set;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        const int r = has ? next[wave * p.E + e] + rank : -1;
+        if (has && (same >> lane) == 1)                // the last of them
+            next[wave * p.E + e] = r + 1;
+        if (i < to)
+            p.position[i] = r;
+        if (has)
+            p.source[r] = i;
+    }
+}
+
+// Pairs up to which the sort is one launch of E + 1 workgroups that all walk the
+// pairs (2048 pairs of 64 experts: 9.7 us, more host time than kernel; two
+// launches 13.0), and how more are cut: every block reads the counts of all.
+constexpr int kSortFew = 2048, kSortBlocks = 64;
+static void sort_blocks(int64_t n, int& per, int& blocks)
+{
+    per = (int)std::max<int64_t>(kSortThreads, ceil_div(ceil_div(n, kSortBlocks), kSortThreads) * kSortThreads);
+    blocks = (int)ceil_div(n, per);
 }
 
 // ---------------------------------------------------------------- rows into order
 struct GatherParams {
     const int32_t* position;
     int64_t T, rows;
-    int k;
+    int k, pieces;
     const char* x[2];
     char* out[2];
     int64_t bytes[2];
 };
 
-// A workgroup takes a token: V bytes a step are read once and written to each of its rows.
-template <class V>
-__device__ __forceinline__ void gather_row(const GatherParams& p, int64_t t, const char* x, char* out, int64_t bytes)
+// Sixteen bytes of any alignment: the memory takes them as they are.
+typedef u32x4_t u32x4_any __attribute__((aligned(1)));
+
+constexpr int kPiece = 4;                              // 16-byte loads of a lane
+
+// A wave reads a piece of a token's row once and writes it to each of the
+// token's rows: `at` holds them, a lane each, -1 for none.
+__device__ __forceinline__ void gather_piece(const char* x, char* out, int64_t bytes, int64_t t, int64_t piece, int k,
+                                             int at, int lane)
 {
-    const V* from = reinterpret_cast<const V*>(x + t * bytes);
-    for (int64_t i = threadIdx.x; i < bytes / (int64_t)sizeof(V); i += 256) {
-        const V v = from[i];
-        for (int j = 0; j < p.k; ++j) {
-            const int64_t r = p.position[t * p.k + j];
-            if (r >= 0 && r < p.rows)
-                reinterpret_cast<V*>(out + r * bytes)[i] = v;
-        }
+    const int64_t items = bytes / 16, first = piece * 64 * kPiece + lane;
+    const char* from = x + t * bytes;
+    u32x4_t v[kPiece];
+#pragma unroll
+    for (int q = 0; q < kPiece; ++q)
+        if (first + 64 * q < items)
+            v[q] = reinterpret_cast<const u32x4_any*>(from)[first + 64 * q];
+    // what is left of the row after its whole 16 bytes
+    const int rest = (int)(bytes & 15);
+    const bool ends = rest && (piece + 1) * 64 * kPiece >= items && lane < rest;
+    const char tail = ends ? from[items * 16 + lane] : (char)0;
+    for (int j = 0; j < k; ++j) {
+        const int r = __builtin_amdgcn_readlane(at, j);
+        if (r < 0)
+            continue;
+        char* to = out + (int64_t)r * bytes;
+#pragma unroll
+        for (int q = 0; q < kPiece; ++q)
+            if (first + 64 * q < items)
+                reinterpret_cast<u32x4_any*>(to)[first + 64 * q] = v[q];
+        if (ends)
+            to[items * 16 + lane] = tail;
     }
+}
+
+// A token's rows for lanes j < k, -1 outside the rows.  Lanes are read (readlane)
+// where the whole wave runs: the compiler may compute what a lane gives where it is
+// used, so under a divergent branch inactive lanes would give anything.
+__device__ __forceinline__ int position_of(const int32_t* position, int64_t t, int k, int64_t rows, int lane)
+{
+    const int at = lane < k ? position[t * k + lane] : -1;
+    return at < rows ? at : -1;
 }
 
 __global__ void __launch_bounds__(256) moe_gather_kernel(GatherParams p)
 {
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x)
-        for (int s = 0; s < 2; ++s) {
-            if (p.bytes[s] == 0)
-                continue;
-            const uintptr_t a = (uintptr_t)p.x[s] | (uintptr_t)p.out[s] | (uintptr_t)p.bytes[s];
-            if (a % 16 == 0)
-                gather_row<u32x4_t>(p, t, p.x[s], p.out[s], p.bytes[s]);
-            else if (a % 4 == 0)
-                gather_row<unsigned>(p, t, p.x[s], p.out[s], p.bytes[s]);
-            else
-                gather_row<unsigned char>(p, t, p.x[s], p.out[s], p.bytes[s]);
-        }
+    const int lane = threadIdx.x & 63;
+    const unsigned units = (unsigned)(p.T * p.pieces);
+    for (unsigned u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < units; u += gridDim.x * 4) {
+        const int64_t t = u / (unsigned)p.pieces, piece = u - t * p.pieces;
+        const int at = position_of(p.position, t, p.k, p.rows, lane);
+        gather_piece(p.x[0], p.out[0], p.bytes[0], t, piece, p.k, at, lane);
+        if (piece == 0 && p.bytes[1] > 0)
+            for (int64_t q = 0; q * 1024 * kPiece < p.bytes[1]; ++q)
+                gather_piece(p.x[1], p.out[1], p.bytes[1], t, q, p.k, at, lane);
+    }
 }
 
 // ---------------------------------------------------------------- rows back
@@ -117,69 +264,192 @@ struct CombineParams {
     void *y, *dx;
     float* dweights;
     int64_t T, rows, H;
-    int k;
+    int k, pieces;
+};
+
+// A lane's 16 bytes of a row as fp32: 8 bf16 or 4 fp32, from element h on; those
+// past H are zero and are not written.
+template <bool BF16>
+struct Slice {
+    static constexpr int N = BF16 ? 8 : 4;
+    float v[N];
+    __device__ __forceinline__ void load(const void* row, int64_t h, int64_t H)
+    {
+        if (h + N <= H) {
+            if constexpr (BF16) {
+                const u32x4_t w = *reinterpret_cast<const u32x4_any*>(static_cast<const unsigned short*>(row) + h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
+            } else {
+                const u32x4_t w = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(row) + h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = __uint_as_float(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[i] = 0.0f;
+                if (h + i < H) {
+                    if constexpr (BF16)
+                        v[i] = __uint_as_float((unsigned)static_cast<const unsigned short*>(row)[h + i] << 16);
+                    else
+                        v[i] = static_cast<const float*>(row)[h + i];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void* row, int64_t h, int64_t H) const
+    {
+        if (h + N <= H) {
+            u32x4_t w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (BF16)
+                    w[i] = f32_to_bf16_rne(v[2 * i]) | (unsigned)f32_to_bf16_rne(v[2 * i + 1]) << 16;
+                else
+                    w[i] = __float_as_uint(v[i]);
+            }
+            if constexpr (BF16)
+                *reinterpret_cast<u32x4_any*>(static_cast<unsigned short*>(row) + h) = w;
+            else
+                *reinterpret_cast<u32x4_any*>(static_cast<float*>(row) + h) = w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (h + i < H) {
+                    if constexpr (BF16)
+                        static_cast<unsigned short*>(row)[h + i] = f32_to_bf16_rne(v[i]);
+                    else
+                        static_cast<float*>(row)[h + i] = v[i];
+                }
+        }
+    }
+};
+
+// The same and their weights as scalars.
+template <int KM>
+struct Rows {
+    int r[KM];
+    float w[KM];
+    __device__ __forceinline__ Rows(const CombineParams& p, int64_t t, int lane)
+    {
+        const int at = position_of(p.position, t, p.k, p.rows, lane);
+        const float wl = p.weights && lane < p.k ? p.weights[t * p.k + lane] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            r[j] = __builtin_amdgcn_readlane(at, j);   // -1 from lanes k, k + 1, ..
+            w[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), j));
+        }
+    }
 };
 
 template <bool BF16>
-__device__ __forceinline__ float element(const void* p, int64_t i)
+__device__ __forceinline__ char* row_at(const void* base, int64_t r, int64_t H)
 {
-    if constexpr (BF16)
-        return __uint_as_float((unsigned)static_cast<const unsigned short*>(p)[i] << 16);
-    else
-        return static_cast<const float*>(p)[i];
+    return const_cast<char*>(static_cast<const char*>(base)) + r * H * (BF16 ? 2 : 4);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void put(void* p, int64_t i, float v)
-{
-    if constexpr (BF16)
-        static_cast<unsigned short*>(p)[i] = f32_to_bf16_rne(v);
-    else
-        static_cast<float*>(p)[i] = v;
-}
-
-template <bool BF16>
+// A wave takes 1 KiB of a token's row: up to KM rows' parts are on their way at once.
+template <bool BF16, int KM>
 __global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
 {
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x)
-        for (int64_t h = threadIdx.x; h < p.H; h += 256) {
-            float v = 0.0f;
-            for (int j = 0; j < p.k; ++j) {
-                const int64_t r = p.position[t * p.k + j];
-                if (r >= 0 && r < p.rows)
-                    v = fmaf(p.weights ? p.weights[t * p.k + j] : 1.0f, element<BF16>(p.x, r * p.H + h), v);
-            }
-            put<BF16>(p.y, t * p.H + h, v);
+    using S = Slice<BF16>;
+    const int lane = threadIdx.x & 63;
+    const unsigned units = (unsigned)(p.T * p.pieces);
+    for (unsigned u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < units; u += gridDim.x * 4) {
+        const int64_t t = u / (unsigned)p.pieces, h = (u - t * p.pieces) * 64 * S::N + lane * S::N;
+        const Rows<KM> rows(p, t, lane);
+        S x[KM];
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+            if (rows.r[j] >= 0)
+                x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+        S y;
+#pragma unroll
+        for (int i = 0; i < S::N; ++i)
+            y.v[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+            if (rows.r[j] >= 0)
+#pragma unroll
+                for (int i = 0; i < S::N; ++i)
+                    y.v[i] = fmaf(rows.w[j], x[j].v[i], y.v[i]);
+        y.store(row_at<BF16>(p.y, t, p.H), h, p.H);
+    }
+}
+
+// A workgroup takes a token: dy is read once, each of its rows once, and the k
+// dot products meet at the end.
+template <bool BF16, int KM>
+__global__ void __launch_bounds__(256) moe_combine_grad_kernel(CombineParams p)
+{
+    using S = Slice<BF16>;
+    __shared__ float part[4][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const Rows<KM> rows(p, t, lane);
+        float dot[KM] = {};
+        // the whole workgroup runs every step; threads past H load zeros and store nothing
+        for (int64_t h0 = 0; h0 < p.H; h0 += 256 * S::N) {
+            const int64_t h = h0 + threadIdx.x * S::N;
+            S dy, x[KM];
+            dy.load(row_at<BF16>(p.dy, t, p.H), h, p.H);
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (rows.r[j] >= 0)
+                    x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (rows.r[j] >= 0) {
+                    S d;
+#pragma unroll
+                    for (int i = 0; i < S::N; ++i) {
+                        dot[j] = fmaf(dy.v[i], x[j].v[i], dot[j]);
+                        d.v[i] = rows.w[j] * dy.v[i];
+                    }
+                    d.store(row_at<BF16>(p.dx, rows.r[j], p.H), h, p.H);
+                }
         }
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1)
+                dot[j] += __shfl_xor(dot[j], off);
+            if (lane == 0)
+                part[wave][j] = dot[j];
+        }
+        __syncthreads();
+        if (threadIdx.x < (unsigned)p.k)
+            p.dweights[t * p.k + threadIdx.x] =
+                part[0][threadIdx.x] + part[1][threadIdx.x] + part[2][threadIdx.x] + part[3][threadIdx.x];
+        __syncthreads();
+    }
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(256) moe_combine_grad_kernel(CombineParams p)
+static void launch_combine(const CombineParams& p, unsigned grid, hipStream_t s)
 {
-    __shared__ float part[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x)
-        for (int j = 0; j < p.k; ++j) {
-            const int64_t r = p.position[t * p.k + j];
-            float dot = 0.0f;
-            if (r >= 0 && r < p.rows) {
-                const float w = p.weights[t * p.k + j];
-                for (int64_t h = threadIdx.x; h < p.H; h += 256) {
-                    const float d = element<BF16>(p.dy, t * p.H + h);
-                    dot = fmaf(d, element<BF16>(p.x, r * p.H + h), dot);
-                    put<BF16>(p.dx, r * p.H + h, w * d);
-                }
-            }
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1)
-                dot += __shfl_xor(dot, off);
-            __syncthreads();
-            if (lane == 0)
-                part[wave] = dot;
-            __syncthreads();
-            if (threadIdx.x == 0)
-                p.dweights[t * p.k + j] = part[0] + part[1] + part[2] + part[3];
-        }
+    if (p.k <= 4)
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, 4>), dim3(grid), dim3(256), 0, s, p);
+    else if (p.k <= 8)
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, 8>), dim3(grid), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, 16>), dim3(grid), dim3(256), 0, s, p);
+}
+
+template <bool BF16>
+static void launch_combine_grad(const CombineParams& p, unsigned grid, hipStream_t s)
+{
+    if (p.k <= 4)
+        hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, 4>), dim3(grid), dim3(256), 0, s, p);
+    else if (p.k <= 8)
+        hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, 8>), dim3(grid), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, 16>), dim3(grid), dim3(256), 0, s, p);
 }
 
 // ---------------------------------------------------------------- checks
@@ -247,24 +517,38 @@ int tg_moe_sort_workspace_bytes(int64_t T, int64_t E, int k, size_t* bytes)
         return st;
     if (!bytes)
         return set_error(TG_E_INVAL, "bytes is NULL");
-    *bytes = 0;
+    int per, blocks;
+    sort_blocks(T * k, per, blocks);
+    *bytes = T * k <= kSortFew ? 0 : (size_t)blocks * (size_t)E * 4;
     return TG_OK;
 }
 
 int tg_moe_sort(int64_t T, int64_t E, int k, const int32_t* ids, int32_t* position, int32_t* source,
                 int32_t* offsets, void* workspace, size_t workspace_bytes)
 {
-    (void)workspace, (void)workspace_bytes;
     const int st = check_sort(T, E, k);
     if (st != TG_OK)
         return st;
+    const int64_t n = T * k;
+    SortParams p{ids, position, source, offsets, static_cast<int32_t*>(workspace), (int)n, (int)E, 0, 0};
+    sort_blocks(n, p.per, p.blocks);
+    if (n > kSortFew &&
+        (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < (size_t)p.blocks * (size_t)E * 4))
+        return set_error(TG_E_INVAL,
+                         "the workspace must be 16-byte aligned and hold tg_moe_sort_workspace_bytes() bytes");
     if (!offsets || (T > 0 && (!ids || !position || !source)) ||
         (((uintptr_t)ids | (uintptr_t)position | (uintptr_t)source | (uintptr_t)offsets) & 3u))
         return set_error(TG_E_INVAL, "ids, position, source and offsets must be given, 4-byte aligned");
     if (!have_device())
         return set_error(TG_E_UNSUPPORTED, "no HIP device");
-    hipLaunchKernelGGL(moe_sort_kernel, dim3((unsigned)E + 1), dim3(256), 0, current_stream(), ids, T * k, (int)E,
-                       position, source, offsets);
+    if (n <= kSortFew) {
+        hipLaunchKernelGGL(moe_sort_few_kernel, dim3((unsigned)E + 1), dim3(256), 0, current_stream(), ids, (int)n,
+                           (int)E, position, source, offsets);
+    } else {
+        const dim3 grid((unsigned)p.blocks), block(kSortThreads);
+        hipLaunchKernelGGL(moe_count_kernel, grid, block, 0, current_stream(), p);
+        hipLaunchKernelGGL(moe_place_kernel, grid, block, kSortWaves * (size_t)E * 4, current_stream(), p);
+    }
     return launched("moe_sort launch");
 }
 
@@ -284,9 +568,12 @@ int tg_moe_gather(int64_t T, int k, int64_t rows, const int32_t* position, int64
         return set_error(TG_E_INVAL, "x and out must be given");
     if (!have_device())
         return set_error(TG_E_UNSUPPORTED, "no HIP device");
-    const GatherParams p{position, T, rows, k, {static_cast<const char*>(x), static_cast<const char*>(x2)},
+    const int pieces = (int)std::max<int64_t>(1, ceil_div(row_bytes / 16, 64 * kPiece));
+    if (T * pieces > kUnits)
+        return set_error(TG_E_UNSUPPORTED, "moe_gather: more than 2^31 pieces of 4 KiB");
+    const GatherParams p{position, T, rows, k, pieces, {static_cast<const char*>(x), static_cast<const char*>(x2)},
                          {static_cast<char*>(out), static_cast<char*>(out2)}, {row_bytes, row2_bytes}};
-    hipLaunchKernelGGL(moe_gather_kernel, dim3(grid_of(T)), dim3(256), 0, current_stream(), p);
+    hipLaunchKernelGGL(moe_gather_kernel, dim3(grid_of(ceil_div(T * pieces, 4))), dim3(256), 0, current_stream(), p);
     return launched("moe_gather launch");
 }
 
@@ -301,11 +588,12 @@ int tg_moe_combine(int64_t T, int k, int64_t rows, int64_t H, const void* x, int
         return set_error(TG_E_INVAL, "x and y must be given; x, y and weights aligned to their elements");
     if (!have_device())
         return set_error(TG_E_UNSUPPORTED, "no HIP device");
-    const CombineParams p{x, nullptr, position, weights, y, nullptr, nullptr, T, rows, H, k};
-    if (dtype == TG_BF16)
-        hipLaunchKernelGGL(moe_combine_kernel<true>, dim3(grid_of(T)), dim3(256), 0, current_stream(), p);
-    else
-        hipLaunchKernelGGL(moe_combine_kernel<false>, dim3(grid_of(T)), dim3(256), 0, current_stream(), p);
+    const CombineParams p{x, nullptr, position, weights, y, nullptr, nullptr, T, rows, H, k,
+                          (int)ceil_div(H, dtype == TG_BF16 ? 512 : 256)};
+    if (T * p.pieces > kUnits)
+        return set_error(TG_E_UNSUPPORTED, "moe_combine: more than 2^31 pieces of 1 KiB");
+    const unsigned grid = grid_of(ceil_div(T * p.pieces, 4));
+    dtype == TG_BF16 ? launch_combine<true>(p, grid, current_stream()) : launch_combine<false>(p, grid, current_stream());
     return launched("moe_combine launch");
 }
 
@@ -321,11 +609,9 @@ int tg_moe_combine_grad(int64_t T, int k, int64_t rows, int64_t H, const void* d
         return set_error(TG_E_INVAL, "dy, x, weights, dx and dweights must be given, aligned to their elements");
     if (!have_device())
         return set_error(TG_E_UNSUPPORTED, "no HIP device");
-    const CombineParams p{x, dy, position, weights, nullptr, dx, dweights, T, rows, H, k};
-    if (dtype == TG_BF16)
-        hipLaunchKernelGGL(moe_combine_grad_kernel<true>, dim3(grid_of(T)), dim3(256), 0, current_stream(), p);
-    else
-        hipLaunchKernelGGL(moe_combine_grad_kernel<false>, dim3(grid_of(T)), dim3(256), 0, current_stream(), p);
+    const CombineParams p{x, dy, position, weights, nullptr, dx, dweights, T, rows, H, k, 0};
+    dtype == TG_BF16 ? launch_combine_grad<true>(p, grid_of(T), current_stream())
+                     : launch_combine_grad<false>(p, grid_of(T), current_stream());
     return launched("moe_combine_grad launch");
 }
 
