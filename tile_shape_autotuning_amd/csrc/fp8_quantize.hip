@@ -5,9 +5,13 @@
 //   even, at most 448; 0 where s is 0.  The quotient is rounded as if exact: an
 //   estimate x * (1 / s) is off by at most 2^-23 of its value, so where both ends
 //   of the estimate +- 2^-22 have the same code it is the quotient's; elsewhere
-//   (one element in about 2^17) the quotient is taken in fp64, which cannot fall
-//   on the middle of two codes unless the exact one does (x and the middle times
-//   s have 24 and 29 bits).
+//   (one element in about 2^17) the two codes are neighbours, and the sign of
+//   |x| - t s, t the middle of their values, decides: one FMA gives it exactly (t s
+//   has 29 bits at most).  Scales below 2^-100 are taken times 2^100, with x.
+//
+// Bound by memory: x is read once, into registers, 16 bytes a lane and load at
+// any alignment.  Sixteen lanes have 128 elements of a row.  The transpose's
+// codes, four neighbouring k a thread, cross LDS and leave in whole lines.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -23,132 +27,380 @@ struct F8QuantParams {
     unsigned char* codes;
     float* scales;
     void* values;
+    int64_t rows;                                      // of all matrices
     int64_t R, K;
-    int64_t rs, ks;                                    // elements from one row, one column to the next
+    int64_t works;                                     // workgroups' shares
     int chunks;
 };
 
-constexpr unsigned kInfBits = 0x7F800000u;
+constexpr unsigned kInfBits = 0x7F800000u, kNanBits = 0x7FC00000u;
+typedef u32x4_t u32x4_any __attribute__((aligned(1)));
+typedef unsigned u32x2_t8 __attribute__((ext_vector_type(2)));
+
+// Eight neighbouring elements; those from `n` on are zero and are not written.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&v)[8])
+{
+    if (n >= 8) {
+        if constexpr (BF16) {
+            const u32x4_t w = *reinterpret_cast<const u32x4_any*>(static_cast<const unsigned short*>(base) + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        } else {
+            const u32x4_any* from = reinterpret_cast<const u32x4_any*>(static_cast<const float*>(base) + at);
+            const u32x4_t a = from[0], b = from[1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = __uint_as_float(a[i]);
+                v[4 + i] = __uint_as_float(b[i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 0.0f;
+            if (i < n) {
+                if constexpr (BF16)
+                    v[i] = __uint_as_float((unsigned)static_cast<const unsigned short*>(base)[at + i] << 16);
+                else
+                    v[i] = static_cast<const float*>(base)[at + i];
+            }
+        }
+    }
+}
 
 template <bool BF16>
-__device__ __forceinline__ float load_element(const void* p, int64_t i)
+__device__ __forceinline__ void store8(void* base, int64_t at, int n, const float (&v)[8])
 {
-    if constexpr (BF16)
-        return __uint_as_float((unsigned)static_cast<const unsigned short*>(p)[i] << 16);
-    else
-        return static_cast<const float*>(p)[i];
+    if (n >= 8) {
+        if constexpr (BF16) {
+            u32x4_t w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = f32_to_bf16_rne(v[2 * i]) | (unsigned)f32_to_bf16_rne(v[2 * i + 1]) << 16;
+            *reinterpret_cast<u32x4_any*>(static_cast<unsigned short*>(base) + at) = w;
+        } else {
+            u32x4_any* to = reinterpret_cast<u32x4_any*>(static_cast<float*>(base) + at);
+            to[0] = u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+            to[1] = u32x4_t{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) {
+                if constexpr (BF16)
+                    static_cast<unsigned short*>(base)[at + i] = f32_to_bf16_rne(v[i]);
+                else
+                    static_cast<float*>(base)[at + i] = v[i];
+            }
+    }
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store_element(void* p, int64_t i, float v)
-{
-    if constexpr (BF16)
-        static_cast<unsigned short*>(p)[i] = f32_to_bf16_rne(v);
-    else
-        static_cast<float*>(p)[i] = v;
-}
-
-// A block's scale from the largest |x|, as bits: infinities and NaN are above
-// every number.
-__device__ __forceinline__ float scale_of(unsigned top)
-{
-    return top >= kInfBits ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 448.0f;
-}
-
-// The value of the code nearest to x / s.
-__device__ float nearest_exact(float x, float s)
-{
-    const double q = (double)x / (double)s, a = fabs(q);
-    const int e = max(ilogb(a), -6) - 3;
-    const float r = (float)fmin(ldexp(rint(ldexp(a, -e)), e), 448.0);
-    return copysignf(a == 0.0 ? 0.0f : r, x);
-}
-
-// Code of x with scale s, inv = 1 / s.
-__device__ __forceinline__ unsigned code_of(float x, float s, float inv)
-{
-    if (!(s > 0.0f))
-        return s == 0.0f ? 0u : 0x7Fu;
-    const float q = x * inv;
-    const float lo = __builtin_amdgcn_fmed3f(q * (1.0f - 0x1p-22f), -448.0f, 448.0f);
-    const float hi = __builtin_amdgcn_fmed3f(q * (1.0f + 0x1p-22f), -448.0f, 448.0f);
-    unsigned c = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, 0, false) & 0xFFFFu;
-    // below 2^-100 the reciprocal may overflow, and the quotient is no longer accurate
-    if ((c & 0xFFu) != c >> 8 || s < 0x1p-100f)
-        c = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(nearest_exact(x, s), 0.0f, 0, false);
-    return c & 0xFFu;
-}
-
-__device__ __forceinline__ float value_of(unsigned code, float s)
-{
-    return __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * s;
-}
-
-__device__ __forceinline__ unsigned wave_max_bits(unsigned v)
+// The largest |x| as bits: infinities and NaN are above every number.
+__device__ __forceinline__ unsigned top_of(const float (&v)[8], unsigned top)
 {
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-        v = max(v, (unsigned)__shfl_xor((int)v, off));
-    return v;
+    for (int i = 0; i < 8; ++i)
+        top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return top;
 }
 
-// A workgroup of 256 takes BLOCK rows of one chunk of 128 columns: a wave each
-// for BLOCK = 1, all of them together for 128.
-template <bool BF16, int BLOCK>
-__global__ void __launch_bounds__(256) fp8_quantize_kernel(F8QuantParams p)
+template <int CTRL>
+__device__ __forceinline__ unsigned max_with(unsigned v)
+{
+    return max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
+}
+
+// Over each row of 16 lanes (rotations by 8, 4, 2, 1).
+__device__ __forceinline__ unsigned max16(unsigned v)
+{
+    return max_with<0x121>(max_with<0x122>(max_with<0x124>(max_with<0x128>(v))));
+}
+
+struct Scale {
+    float s;                                           // as stored
+    float t, inv, by;                                  // that x * by is divided by, its reciprocal
+    __device__ __forceinline__ explicit Scale(unsigned top)
+    {
+        s = top >= kInfBits ? __uint_as_float(kNanBits) : __uint_as_float(top) / 448.0f;
+        by = s < 0x1p-100f ? 0x1p100f : 1.0f;
+        t = s * by;
+        inv = t > 0.0f ? 1.0f / t : 0.0f;
+    }
+};
+
+// Codes of four elements whose estimates' ends differ somewhere (lo, hi).
+__device__ __forceinline__ unsigned resolve4(const float* x, const Scale& s, unsigned lo, unsigned hi)
+{
+    unsigned c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned a = lo >> (8 * i) & 0x7Fu, b = hi >> (8 * i) & 0x7Fu;
+        const float va = __builtin_amdgcn_cvt_f32_fp8((int)a, 0), vb = __builtin_amdgcn_cvt_f32_fp8((int)b, 0);
+        const float d = fmaf(-0.5f * (va + vb), s.t, fabsf(x[i] * s.by));
+        const unsigned code = d > 0.0f || (d == 0.0f && (b & 1) == 0) ? b : a;
+        c |= (code | (lo >> (8 * i) & 0x80u)) << (8 * i);
+    }
+    return c;
+}
+
+__device__ __forceinline__ u32x2_t8 encode8(const float (&v)[8], const Scale& s)
+{
+    u32x2_t8 out;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float lo[4], hi[4];
+        const float* x = v + 4 * h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // above 448 only where a subnormal scale was rounded down
+            float q = x[i] * s.inv;
+            if (s.by != 1.0f)
+                q = __builtin_amdgcn_fmed3f((x[i] * s.by) * s.inv, -448.0f, 448.0f);
+            lo[i] = q * (1.0f - 0x1p-22f);
+            hi[i] = q * (1.0f + 0x1p-22f);
+        }
+        const int a = __builtin_amdgcn_cvt_pk_fp8_f32(lo[2], lo[3], __builtin_amdgcn_cvt_pk_fp8_f32(lo[0], lo[1], 0, false), true);
+        const int b = __builtin_amdgcn_cvt_pk_fp8_f32(hi[2], hi[3], __builtin_amdgcn_cvt_pk_fp8_f32(hi[0], hi[1], 0, false), true);
+        out[h] = (unsigned)a;
+        if (a != b)
+            out[h] = resolve4(x, s, (unsigned)a, (unsigned)b);
+        if (!(s.s > 0.0f))
+            out[h] = s.s == 0.0f ? 0u : 0x7F7F7F7Fu;
+    }
+    return out;
+}
+
+// Codes from element n on are zero.
+__device__ __forceinline__ u32x2_t8 first_of(u32x2_t8 c, int n)
+{
+    if (n < 8) {
+        c[1] = n <= 4 ? 0u : c[1] & ((1u << (8 * (n - 4))) - 1);
+        c[0] = n <= 0 ? 0u : n < 4 ? c[0] & ((1u << (8 * n)) - 1) : c[0];
+    }
+    return c;
+}
+
+__device__ __forceinline__ void decode8(u32x2_t8 c, const Scale& s, float (&v)[8])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        v[4 * h] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 0) * s.s;
+        v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 1) * s.s;
+        v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 2) * s.s;
+        v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 3) * s.s;
+    }
+}
+
+// x [R][K].  Sixteen lanes take a chunk of a row.  BLOCK = 1: U of them, each on
+// its own; 128: U = 8, a workgroup's 16 rows eight times over make its block.
+template <bool BF16, int BLOCK, int U>
+__global__ void __launch_bounds__(256) fp8_quantize_along_kernel(F8QuantParams p)
 {
     __shared__ unsigned tops[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t mat = blockIdx.z;
-    const int64_t group = BLOCK == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
-    const int64_t row0 = group * BLOCK, row1 = min(p.R, row0 + BLOCK);
+    const int l16 = threadIdx.x & 15, team = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int64_t Kp = (int64_t)p.chunks * 128;
-    const int64_t base = mat * p.R * p.K;
-    const int first = BLOCK == 1 ? 0 : wave, step = BLOCK == 1 ? 1 : 4;
-    for (int chunk = blockIdx.y; chunk < p.chunks; chunk += gridDim.y) {
-    unsigned top = 0;
-    for (int64_t r = row0 + first; r < row1; r += step)
-        for (int i = 0; i < 2; ++i) {
-            const int64_t k = chunk * 128 + 64 * i + lane;
-            if (k < p.K)
-                top = max(top, __float_as_uint(load_element<BF16>(p.x, base + r * p.rs + k * p.ks)) & 0x7FFFFFFFu);
-        }
-    top = wave_max_bits(top);
-    if constexpr (BLOCK == 128) {
-        if (lane == 0)
-            tops[wave] = top;
-        __syncthreads();
-        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-    }
-    const float s = scale_of(top), inv = 1.0f / s;
-    for (int64_t r = row0 + first; r < row1; r += step)
-        for (int i = 0; i < 2; ++i) {
-            const int64_t k = chunk * 128 + 64 * i + lane;
-            unsigned c = 0;
-            if (k < p.K) {
-                const int64_t at = base + r * p.rs + k * p.ks;
-                c = code_of(load_element<BF16>(p.x, at), s, inv);
-                if (p.values)
-                    store_element<BF16>(p.values, at, value_of(c, s));
+    for (int64_t work = blockIdx.x; work < p.works; work += gridDim.x) {
+        int64_t row[U], block = 0;
+        int chunk[U];
+        if constexpr (BLOCK == 1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const unsigned g = (unsigned)(work * U + u) * 16 + team;
+                row[u] = g / (unsigned)p.chunks;
+                chunk[u] = (int)(g - (unsigned)row[u] * (unsigned)p.chunks);
             }
-            p.codes[(mat * p.R + r) * Kp + k] = (unsigned char)c;
+        } else {
+            const int64_t blocks = (p.R + 127) / 128, rb = work / p.chunks, mat = rb / blocks;
+            block = work;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = (rb - mat * blocks) * 128 + u * 16 + team;
+                row[u] = r < p.R ? mat * p.R + r : p.rows;
+                chunk[u] = (int)(work - rb * p.chunks);
+            }
         }
-    const int64_t groups = (p.R + BLOCK - 1) / BLOCK;
-    if (row0 < p.R && lane == 0 && (BLOCK == 1 || wave == 0))
-        p.scales[(mat * groups + group) * p.chunks + chunk] = s;
-    __syncthreads();
+        float v[U][8];
+        unsigned top[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = chunk[u] * 128 + 8 * l16;
+            load8<BF16>(p.x, row[u] * p.K + k, row[u] < p.rows ? (int)min((int64_t)8, p.K - k) : 0, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            top[u] = top_of(v[u], 0u);
+        if constexpr (BLOCK == 128) {
+#pragma unroll
+            for (int u = 1; u < U; ++u)
+                top[0] = max(top[0], top[u]);
+            unsigned t = max16(top[0]);
+            t = max(t, (unsigned)__shfl_xor((int)t, 16));
+            t = max(t, (unsigned)__shfl_xor((int)t, 32));
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0)
+                tops[wave] = t;
+            __syncthreads();
+            t = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                top[u] = t;
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                top[u] = max16(top[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Scale s(top[u]);
+            const int64_t k = chunk[u] * 128 + 8 * l16;
+            const int n = (int)min((int64_t)8, p.K - k);
+            if (row[u] < p.rows) {
+                const u32x2_t8 c = first_of(encode8(v[u], s), n);
+                *reinterpret_cast<u32x2_t8*>(p.codes + row[u] * Kp + k) = c;
+                if (p.values) {
+                    decode8(c, s, v[u]);
+                    store8<BF16>(p.values, row[u] * p.K + k, n, v[u]);
+                }
+                if (BLOCK == 1 && l16 == 0)
+                    p.scales[row[u] * p.chunks + chunk[u]] = s.s;
+            }
+            if (BLOCK == 128 && u == 0 && threadIdx.x == 0)
+                p.scales[block] = s.s;
+        }
     }
 }
 
-template <bool BF16>
-static int launch_quantize(const F8QuantParams& p, int64_t count, int block, hipStream_t s)
+// x [K][R]: a workgroup takes 128 k of 128 rows, a thread eight neighbouring rows
+// of k = 64 h + 4 (tid / 16) + i, h = 0, 1, i = 0..3.
+template <bool BF16, int BLOCK>
+__global__ void __launch_bounds__(256) fp8_quantize_across_kernel(F8QuantParams p)
 {
-    const dim3 grid((unsigned)ceil_div(p.R, block == 1 ? 4 : 128), (unsigned)std::min(p.chunks, 65535),
-                    (unsigned)count);
-    if (block == 1)
-        hipLaunchKernelGGL((fp8_quantize_kernel<BF16, 1>), grid, dim3(256), 0, s, p);
+    constexpr int PITCH = 33;                          // dwords of a row of codes: threads 16 apart on other banks
+    __shared__ unsigned out[128 * PITCH];
+    __shared__ unsigned tops[BLOCK == 1 ? 4 * 128 : 4];
+    const int l16 = threadIdx.x & 15, team = threadIdx.x >> 4, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t Kp = (int64_t)p.chunks * 128, blocks = (p.R + 127) / 128;
+    for (int64_t work = blockIdx.x; work < p.works; work += gridDim.x) {
+        // neighbouring workgroups read neighbouring rows' parts of the same lines' pages
+        const int64_t mat = work / (blocks * p.chunks), in = work - mat * blocks * p.chunks;
+        const int64_t chunk = in / blocks, rb = in - chunk * blocks;
+        const int64_t r0 = rb * 128 + 8 * l16, k0 = chunk * 128 + 4 * team, base = mat * p.R * p.K;
+        const int n = (int)max((int64_t)0, min((int64_t)8, p.R - r0));
+        float v[8][8];                                 // [h, i][row]
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int64_t k = k0 + 64 * (q >> 2) + (q & 3);
+            load8<BF16>(p.x, base + k * p.R + r0, k < p.K ? n : 0, v[q]);
+        }
+        unsigned top[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            top[e] = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                top[e] = max(top[e], __float_as_uint(v[q][e]) & 0x7FFFFFFFu);
+            top[e] = max(top[e], (unsigned)__shfl_xor((int)top[e], 16));
+            top[e] = max(top[e], (unsigned)__shfl_xor((int)top[e], 32));
+        }
+        __syncthreads();                               // the last work's codes and tops are read
+        if constexpr (BLOCK == 1) {
+            if (lane < 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    tops[wave * 128 + 8 * l16 + e] = top[e];
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = 8 * l16 + e;
+                top[e] = max(max(tops[r], tops[128 + r]), max(tops[256 + r], tops[384 + r]));
+            }
+        } else {
+            unsigned t = top[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e)
+                t = max(t, top[e]);
+            t = max16(t);
+            if (lane == 0)
+                tops[wave] = t;
+            __syncthreads();
+            t = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                top[e] = t;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const Scale s(top[e]);
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                x[q] = v[q][e];
+            u32x2_t8 c = encode8(x, s);
+            // k past K
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t left = p.K - (k0 + 64 * h);
+                c[h] = left <= 0 ? 0u : left < 4 ? c[h] & ((1u << (8 * (int)left)) - 1) : c[h];
+                out[(8 * l16 + e) * PITCH + 16 * h + team] = c[h];
+            }
+            if (p.values) {
+                decode8(c, s, x);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    v[q][e] = x[q];
+            }
+            if (BLOCK == 1 && team == 0 && e < n)
+                p.scales[(mat * p.R + r0 + e) * p.chunks + chunk] = s.s;
+            if (BLOCK == 128 && e == 0 && threadIdx.x == 0)
+                p.scales[(mat * blocks + rb) * p.chunks + chunk] = s.s;
+        }
+        if (p.values) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int64_t k = k0 + 64 * (q >> 2) + (q & 3);
+                store8<BF16>(p.values, base + k * p.R + r0, k < p.K ? n : 0, v[q]);
+            }
+        }
+        __syncthreads();
+        // eight threads a row, sixteen codes each
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = q * 32 + (threadIdx.x >> 3), at = r * PITCH + 4 * (threadIdx.x & 7);
+            if (rb * 128 + r < p.R)
+                *reinterpret_cast<u32x4_t*>(p.codes + (mat * p.R + rb * 128 + r) * Kp + chunk * 128 +
+                                            16 * (threadIdx.x & 7)) = u32x4_t{out[at], out[at + 1], out[at + 2], out[at + 3]};
+        }
+    }
+}
+
+// Chunks of rows from which a lane takes four at a time (fewer fill the compute
+// units only one by one).
+constexpr int64_t kManyChunks = (int64_t)1 << 16;
+
+template <bool BF16>
+static int launch_quantize(F8QuantParams p, int64_t count, int block, bool along, hipStream_t s)
+{
+    const int64_t blocks = count * ceil_div(p.R, 128) * p.chunks, chunks = p.rows * p.chunks;
+    if (block == 1 && along && chunks > 0xFFFFFF00ll)
+        return set_error(TG_E_UNSUPPORTED, "fp8_quantize: more than 2^32 chunks of 128 elements");
+    auto grid = [&](int64_t works) {
+        p.works = works;
+        return dim3((unsigned)std::min<int64_t>(works, 1 << 22));
+    };
+    if (!along && block == 1)
+        hipLaunchKernelGGL((fp8_quantize_across_kernel<BF16, 1>), grid(blocks), dim3(256), 0, s, p);
+    else if (!along)
+        hipLaunchKernelGGL((fp8_quantize_across_kernel<BF16, 128>), grid(blocks), dim3(256), 0, s, p);
+    else if (block == 128)
+        hipLaunchKernelGGL((fp8_quantize_along_kernel<BF16, 128, 8>), grid(blocks), dim3(256), 0, s, p);
+    else if (chunks < kManyChunks)
+        hipLaunchKernelGGL((fp8_quantize_along_kernel<BF16, 1, 1>), grid(ceil_div(chunks, 16)), dim3(256), 0, s, p);
     else
-        hipLaunchKernelGGL((fp8_quantize_kernel<BF16, 128>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((fp8_quantize_along_kernel<BF16, 1, 4>), grid(ceil_div(chunks, 64)), dim3(256), 0, s, p);
     return launched("fp8_quantize launch");
 }
 
@@ -182,13 +434,12 @@ int tg_fp8_quantize(int64_t count, int64_t R, int64_t K, int block, const void* 
     p.codes = static_cast<unsigned char*>(codes);
     p.scales = scales;
     p.values = values;
+    p.rows = count * R;
     p.R = R;
     p.K = K;
-    p.rs = rows_first ? K : 1;
-    p.ks = rows_first ? 1 : R;
     p.chunks = (int)ceil_div(K, 128);
-    return dtype == TG_BF16 ? launch_quantize<true>(p, count, block, current_stream())
-                            : launch_quantize<false>(p, count, block, current_stream());
+    return dtype == TG_BF16 ? launch_quantize<true>(p, count, block, rows_first != 0, current_stream())
+                            : launch_quantize<false>(p, count, block, rows_first != 0, current_stream());
 }
 
 }  // extern "C"
