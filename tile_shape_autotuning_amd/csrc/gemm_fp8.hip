@@ -6,8 +6,8 @@
 // A chunk of 128 k of 16 x 16 results is summed from zero; a lane's four sums are
 // multiplied by their scales as they are added up, in fp32.  B is the first
 // operand: a lane then has one row m and four neighbouring columns n.  fp32
-// results take the exact form of the products, bf16 results of many rows the
-// fast one (fp8.hpp).
+// results and few rows take the exact form of the products, bf16 results of many
+// rows the fast one (fp8.hpp).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -53,83 +53,51 @@ __device__ __forceinline__ int expert_tiles(const F8Params& p, int e, int lane, 
     return n;
 }
 
+// The workgroup's tile of the experts' products: rows [m0, m1) of expert
+// `expert` (BM of them at most matter), column tile tn.  Tiles are numbered expert
+// by expert, column tiles of a row tile in order, and each XCD has a contiguous
+// range.  False past the last tile: the grid is for as many as there can be.  Every
+// wave works it out by itself; all of its lanes run.
+template <int BM>
+__device__ __forceinline__ bool expert_tile(const F8Params& p, int tiles_n, int64_t& m0, int64_t& m1, int& tn,
+                                            int& expert)
+{
+    const int lane = threadIdx.x & 63;
+    int total = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        int64_t lo, hi;
+        total += __builtin_amdgcn_readlane(expert_tiles<BM>(p, e0 + lane, lane, lo, hi), 63);
+    }
+    const int64_t n = (int64_t)total * tiles_n, q = n >> 3, r = n & 7;
+    const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    if (i >= q + (x < r ? 1 : 0))
+        return false;
+    const int64_t id = x * q + min(x, r) + i;
+    int tile = (int)(id / tiles_n);
+    tn = (int)(id - (int64_t)tile * tiles_n);
+    for (int e0 = 0;; e0 += 64) {
+        int64_t lo, hi;
+        const int upto = expert_tiles<BM>(p, e0 + lane, lane, lo, hi);
+        const int here = __builtin_amdgcn_readlane(upto, 63);
+        if (tile >= here) {
+            tile -= here;
+            continue;
+        }
+        const int at = __ffsll((long long)__ballot(upto > tile)) - 1;
+        const int before = at ? __builtin_amdgcn_readlane(upto, at - 1) : 0;
+        expert = e0 + at;
+        m0 = (int64_t)__builtin_amdgcn_readlane((int)lo, at) + (int64_t)(tile - before) * BM;
+        m1 = __builtin_amdgcn_readlane((int)hi, at);
+        return true;
+    }
+}
+
 }  // namespace tg
 
+#include "gemm_fp8_stream.hpp"
 #include "gemm_fp8_tiles.hpp"
 
 namespace tg {
-
-// The rows [begin, end) and the matrix of B that row tile `tile` of BM rows
-// belongs to; false past the last tile.
-template <int BM>
-__device__ __forceinline__ bool rows_of_tile(const F8Params& p, int64_t tile, int64_t& begin, int64_t& end, int& expert)
-{
-    if (!p.offsets) {
-        begin = tile * BM;
-        end = p.M;
-        expert = 0;
-        return begin < p.M;
-    }
-    for (int e = 0; e < p.E; ++e) {
-        const int64_t lo = max((int64_t)0, (int64_t)p.offsets[e]), hi = min(p.M, (int64_t)p.offsets[e + 1]);
-        const int64_t tiles = hi > lo ? (hi - lo + BM - 1) / BM : 0;
-        if (tile < tiles) {
-            begin = lo + tile * BM;
-            end = hi;
-            expert = e;
-            return true;
-        }
-        tile -= tiles;
-    }
-    return false;
-}
-
-// A wave takes 16 rows and 64 columns.
-__global__ void __launch_bounds__(256) gemm_fp8_kernel(F8Params p)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int l16 = lane & 15, g = lane >> 4;
-    int64_t m0, m1;
-    int expert;
-    if (!rows_of_tile<16>(p, blockIdx.x, m0, m1, expert))
-        return;
-    const int64_t Kp = (int64_t)p.chunks * 128;
-    const int64_t groups = (p.N + p.b_rows - 1) / p.b_rows;
-    const unsigned char* B = p.B + (int64_t)expert * p.N * Kp;
-    const float* sB = p.sB + (int64_t)expert * groups * p.chunks;
-    for (int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 64; n0 < p.N; n0 += (int64_t)gridDim.y * 256) {
-        const int64_t m = min(m0 + l16, m1 - 1);
-        f32x4_t acc[4] = {};
-        for (int c = 0; c < p.chunks; ++c) {
-            const u32x4_t* a = reinterpret_cast<const u32x4_t*>(p.A + m * Kp + c * 128);
-            const Expanded af = expand(a[g], a[g + 4]);
-            const float sa = p.sA[m * p.chunks + c];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = min(n0 + 16 * j + l16, p.N - 1);
-                const u32x4_t* b = reinterpret_cast<const u32x4_t*>(B + n * Kp + c * 128);
-                const f32x4_t d = mfma_exact(expand(b[g], b[g + 4]), af);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t nn = min(n0 + 16 * j + 4 * g + i, p.N - 1);
-                    acc[j][i] = fmaf(d[i], sa * sB[nn / p.b_rows * p.chunks + c], acc[j][i]);
-                }
-            }
-        }
-        if (m0 + l16 < m1)
-            for (int j = 0; j < 4; ++j)
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t n = n0 + 16 * j + 4 * g + i;
-                    if (n < p.N) {
-                        const float v = apply_act(acc[j][i] + (p.bias ? p.bias[n] : 0.0f), p.act);
-                        if (p.out_bf16)
-                            static_cast<unsigned short*>(p.C)[(m0 + l16) * p.N + n] = f32_to_bf16_rne(v);
-                        else
-                            static_cast<float*>(p.C)[(m0 + l16) * p.N + n] = v;
-                    }
-                }
-    }
-}
 
 template <int BM, int BN, int WGM, int WGN, bool BROWS, bool EXACT>
 static int launch_tiles(const F8Params& p, hipStream_t s)
@@ -141,21 +109,55 @@ static int launch_tiles(const F8Params& p, hipStream_t s)
     return launched("gemm_fp8 launch");
 }
 
+template <int MT, int P, int R, int W, bool BROWS>
+static int launch_stream(const F8Params& p, hipStream_t s)
+{
+    const int64_t tiles_m = p.offsets ? ceil_div(p.M, 16 * MT) + std::min<int64_t>(p.E, p.M) : 1;
+    hipLaunchKernelGGL((gemm_fp8_stream_kernel<MT, P, R, W, BROWS>), dim3((unsigned)(tiles_m * ceil_div(p.N, 16 * P))),
+                       dim3(64 * W), (F8Stream<MT, P, R, W, BROWS>::LDS), s, p);
+    return launched("gemm_fp8 launch");
+}
+
+// Panels a workgroup, depth of the ring and waves: where there are many panels
+// several of them share the rows' traffic, where there are few each gets a
+// workgroup, and many waves, to itself (16 x 28672 x 8192: eight panels 44 us, one
+// 64; 1 x 4096 x 4096: one panel 5.6, eight 20).  Experts have about `rows` rows
+// each, often fewer: one or two tiles of 16, and two waves, so that a compute unit
+// holds several workgroups (64 tokens over 64 experts of 2816 x 2048 63 us, with
+// four waves 72; 256 tokens: two tiles 83, one 94).
+constexpr int64_t kStreamRows = 64;
+template <bool BROWS>
+static int stream_by_rows(const F8Params& p, int64_t rows, hipStream_t s)
+{
+    const int64_t panels = ceil_div(p.N, 16);
+    if (p.offsets) {
+        const int64_t works = panels * std::min<int64_t>(p.E, p.M);
+        if (works < 512)
+            return launch_stream<1, 1, 2, 8, BROWS>(p, s);
+        return rows <= 8 ? launch_stream<1, 4, 2, 2, BROWS>(p, s) : launch_stream<2, 4, 2, 2, BROWS>(p, s);
+    }
+    if (rows <= 16)
+        return panels < 512 ? launch_stream<1, 1, 2, 8, BROWS>(p, s)
+                            : panels < 1536 ? launch_stream<1, 4, 2, 4, BROWS>(p, s)
+                                            : launch_stream<1, 8, 2, 4, BROWS>(p, s);
+    if (rows <= 32)
+        return panels < 512 ? launch_stream<2, 1, 3, 4, BROWS>(p, s) : launch_stream<2, 4, 2, 4, BROWS>(p, s);
+    return panels < 512 ? launch_stream<4, 1, 2, 4, BROWS>(p, s) : launch_stream<4, 4, 1, 4, BROWS>(p, s);
+}
+
 static int launch_gemm(F8Params p, hipStream_t s)
 {
     p.group_m = 8;
     p.vec_out = p.N % 4 == 0 && (uintptr_t)p.C % (p.out_bf16 ? 8 : 16) == 0;
-    if (p.M > 64) {
-        if (p.out_bf16)
-            return p.b_rows == 1 ? launch_tiles<256, 256, 2, 4, true, false>(p, s)
-                                 : launch_tiles<256, 256, 2, 4, false, false>(p, s);
-        return p.b_rows == 1 ? launch_tiles<128, 128, 2, 2, true, true>(p, s)
-                             : launch_tiles<128, 128, 2, 2, false, true>(p, s);
-    }
-    const int64_t tiles = ceil_div(p.M, 16) + (p.offsets ? p.E : 0);
-    hipLaunchKernelGGL(gemm_fp8_kernel, dim3((unsigned)tiles, (unsigned)std::min<int64_t>(ceil_div(p.N, 256), 65535)),
-                       dim3(256), 0, s, p);
-    return launched("gemm_fp8 launch");
+    // rows that a workgroup of the streaming kernel would have
+    const int64_t rows = p.offsets ? ceil_div(p.M, std::min<int64_t>(p.E, p.M)) : p.M;
+    if (rows <= kStreamRows)
+        return p.b_rows == 1 ? stream_by_rows<true>(p, rows, s) : stream_by_rows<false>(p, rows, s);
+    if (p.out_bf16)
+        return p.b_rows == 1 ? launch_tiles<256, 256, 2, 4, true, false>(p, s)
+                             : launch_tiles<256, 256, 2, 4, false, false>(p, s);
+    return p.b_rows == 1 ? launch_tiles<128, 128, 2, 2, true, true>(p, s)
+                         : launch_tiles<128, 128, 2, 2, false, true>(p, s);
 }
 
 static int check_product(int64_t M, int64_t N, int64_t K, int dtype)

@@ -206,41 +206,12 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, char* lds, int64_t m0
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int col = wn * Cf::WN + 16 * j + 4 * g;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = apply_act(acc[i][j][e] + (p.bias && col + e < cols ? p.bias[n0 + col + e] : 0.0f), p.act);
-            const int64_t at = (m0 + r) * p.N + n0 + col;
-            if (p.out_bf16) {
-                unsigned short* to = static_cast<unsigned short*>(p.C) + at;
-                if (p.vec_out && col < cols) {
-                    typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
-                    *reinterpret_cast<u16x4*>(to) = u16x4{f32_to_bf16_rne(v[0]), f32_to_bf16_rne(v[1]),
-                                                          f32_to_bf16_rne(v[2]), f32_to_bf16_rne(v[3])};
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < cols)
-                            to[e] = f32_to_bf16_rne(v[e]);
-                }
-            } else {
-                float* to = static_cast<float*>(p.C) + at;
-                if (p.vec_out && col < cols) {
-                    *reinterpret_cast<f32x4_t*>(to) = f32x4_t{v[0], v[1], v[2], v[3]};
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < cols)
-                            to[e] = v[e];
-                }
-            }
+            if (col < cols)
+                store_results(p, m0 + r, n0 + col, acc[i][j]);
         }
     }
 }
 
-// Tile number `id` of the grid, renumbered so that each XCD has a contiguous
-// range: row tile and column tile, neighbours share rows of A or, in groups of
-// `group_m` row tiles, columns of B.
 template <int BM, int BN, int WGM, int WGN, bool BROWS, bool EXACT>
 __global__ void __launch_bounds__(64 * WGM * WGN, 2) gemm_fp8_tiles_kernel(F8Params p)
 {
@@ -249,35 +220,8 @@ __global__ void __launch_bounds__(64 * WGM * WGN, 2) gemm_fp8_tiles_kernel(F8Par
     int64_t m0, m1;
     int tn, expert = 0;
     if (p.offsets) {
-        // every wave finds its tile: a lane counts the row tiles of experts lane, lane + 64, ..
-        const int lane = threadIdx.x & 63;
-        int total = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 64) {
-            int64_t lo, hi;
-            total += __builtin_amdgcn_readlane(expert_tiles<BM>(p, e0 + lane, lane, lo, hi), 63);
-        }
-        const int64_t n = (int64_t)total * tiles_n, q = n >> 3, r = n & 7;
-        const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
-        if (i >= q + (x < r ? 1 : 0))
+        if (!expert_tile<BM>(p, tiles_n, m0, m1, tn, expert))
             return;
-        const int64_t logical = x * q + min(x, r) + i;
-        int tile = (int)(logical / tiles_n);
-        tn = (int)(logical % tiles_n);
-        for (int e0 = 0;; e0 += 64) {
-            int64_t lo, hi;
-            const int upto = expert_tiles<BM>(p, e0 + lane, lane, lo, hi);
-            const int here = __builtin_amdgcn_readlane(upto, 63);
-            if (tile >= here) {
-                tile -= here;
-                continue;
-            }
-            const int at = __ffsll((long long)__ballot(upto > tile)) - 1;
-            const int before = at ? __builtin_amdgcn_readlane(upto, at - 1) : 0;
-            expert = e0 + at;
-            m0 = (int64_t)__builtin_amdgcn_readlane((int)lo, at) + (int64_t)(tile - before) * BM;
-            m1 = __builtin_amdgcn_readlane((int)hi, at);
-            break;
-        }
     } else {
         const int tiles_m = (int)((p.M + BM - 1) / BM);
         int tile, tm, split;
