@@ -159,7 +159,11 @@ def _integers(rng, R_, K, block, lead=()):
 GEMMS = [(1, 1, 1), (1, 16, 128), (1, 256, 4096), (3, 17, 33), (16, 300, 1000), (17, 64, 256), (33, 257, 513),
          (64, 1001, 777), (65, 80, 128), (100, 48, 2100), (128, 128, 128), (130, 257, 640), (256, 256, 1024),
          (257, 520, 300), (300, 1000, 130), (513, 129, 2048), (2, 3000, 96), (1, 40, 9000), (70, 33, 9000),
-         (1000, 260, 384), (40, 5000, 260), (520, 770, 1280)]
+         (1000, 260, 384), (40, 5000, 260), (520, 770, 1280),
+         # each tile, whole and ragged, and reductions in parts
+         (2050, 8200, 260), (600, 4100, 390), (2048, 2100, 130), (1500, 5000, 260), (3000, 2996, 200), (100, 1000, 9000),
+         (128, 1100, 4100), (300, 4000, 1400), (66, 250, 5000), (200, 100, 2600),
+         (2706, 2903, 100), (2852, 666, 100), (395, 900, 2600), (72, 4157, 5000), (1060, 192, 5000), (1607, 283, 5000)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMMS)
@@ -202,7 +206,7 @@ def _cut(a, b):
     return 7 * 2.0 ** -13 * (np.abs(a) @ np.abs(b).T)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (40, 130, 777), (200, 257, 1500), (300, 512, 4096), (64, 64, 20000)])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (40, 130, 777), (200, 257, 1500), (300, 512, 4096), (64, 64, 20000), (70, 64, 20000)])
 @pytest.mark.parametrize("block", [1, 128])
 def test_gemm_within_the_bound_of_its_sums(M, N, K, block):
     rng = np.random.default_rng(M + K)
@@ -427,7 +431,8 @@ def test_combine_gradient_agrees_with_differences():
 EXPERTS = [(1, 8, 2, 64, 128, "plain"), (5, 16, 4, 100, 200, "away"), (64, 8, 2, 257, 300, "plain"),
            (200, 5, 2, 130, 520, "repeats"), (300, 4, 1, 513, 128, "one"), (30, 64, 6, 96, 384, "plain"),
            (40, 3, 2, 33, 129, "none"), (700, 6, 3, 256, 256, "away"), (1200, 3, 2, 300, 640, "plain"),
-           (2, 300, 1, 40, 140, "plain"), (130, 2, 1, 520, 1024, "plain")]
+           (2, 300, 1, 40, 140, "plain"), (130, 2, 1, 520, 1024, "plain"), (2000, 4, 2, 1200, 260, "away"),
+           (1500, 8, 2, 550, 130, "plain"), (900, 70, 3, 130, 200, "away"), (1, 2, 1, 9000, 300, "plain")]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,kind", EXPERTS)

@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <string>
 
 #include "fp8.hpp"
@@ -18,6 +19,7 @@
 
 namespace tg {
 
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;       // of at most 512 threads: a grid has 2^32 threads
 constexpr int64_t kMaxDepth = (int64_t)1 << 22;        // 256 rows of A or B stay within 32-bit offsets
 
 struct F8Params {
@@ -32,6 +34,9 @@ struct F8Params {
     int out_bf16, act;
     int vec_out;                                       // four results of a row are one aligned access
     int group_m;                                       // row tiles that go through the column tiles together
+    int split, each;                                   // parts of the reduction, chunks of one
+    float* slabs;                                      // their sums, `slab` floats apart
+    int64_t slab;
 };
 
 // How many tiles of BM rows the experts up to `e` of its group of 64 have (lane
@@ -99,13 +104,16 @@ __device__ __forceinline__ bool expert_tile(const F8Params& p, int tiles_n, int6
 
 namespace tg {
 
-template <int BM, int BN, int WGM, int WGN, bool BROWS, bool EXACT>
+template <int BM, int BN, int WGM, int WGN, int ST, bool BROWS, bool EXACT>
 static int launch_tiles(const F8Params& p, hipStream_t s)
 {
-    using Cf = F8Tile<BM, BN, WGM, WGN, BROWS>;
+    using Cf = F8Tile<BM, BN, WGM, WGN, ST, BROWS>;
     const int64_t tiles_m = ceil_div(p.M, BM) + (p.offsets ? std::min<int64_t>(p.E, p.M) : 0);
-    hipLaunchKernelGGL((gemm_fp8_tiles_kernel<BM, BN, WGM, WGN, BROWS, EXACT>),
-                       dim3((unsigned)(tiles_m * ceil_div(p.N, BN))), dim3(Cf::T), Cf::LDS, s, p);
+    const int64_t blocks = tiles_m * ceil_div(p.N, BN) * std::max(p.split, 1);
+    if (blocks > kMaxBlocks)
+        return set_error(TG_E_UNSUPPORTED, "too many tiles for one launch");
+    hipLaunchKernelGGL((gemm_fp8_tiles_kernel<BM, BN, WGM, WGN, ST, BROWS, EXACT>), dim3((unsigned)blocks), dim3(Cf::T),
+                       Cf::LDS, s, p);
     return launched("gemm_fp8 launch");
 }
 
@@ -113,8 +121,11 @@ template <int MT, int P, int R, int W, bool BROWS>
 static int launch_stream(const F8Params& p, hipStream_t s)
 {
     const int64_t tiles_m = p.offsets ? ceil_div(p.M, 16 * MT) + std::min<int64_t>(p.E, p.M) : 1;
-    hipLaunchKernelGGL((gemm_fp8_stream_kernel<MT, P, R, W, BROWS>), dim3((unsigned)(tiles_m * ceil_div(p.N, 16 * P))),
-                       dim3(64 * W), (F8Stream<MT, P, R, W, BROWS>::LDS), s, p);
+    const int64_t blocks = tiles_m * ceil_div(p.N, 16 * P);
+    if (blocks > kMaxBlocks)
+        return set_error(TG_E_UNSUPPORTED, "too many tiles for one launch");
+    hipLaunchKernelGGL((gemm_fp8_stream_kernel<MT, P, R, W, BROWS>), dim3((unsigned)blocks), dim3(64 * W),
+                       (F8Stream<MT, P, R, W, BROWS>::LDS), s, p);
     return launched("gemm_fp8 launch");
 }
 
@@ -125,7 +136,7 @@ static int launch_stream(const F8Params& p, hipStream_t s)
 // each, often fewer: one or two tiles of 16, and two waves, so that a compute unit
 // holds several workgroups (64 tokens over 64 experts of 2816 x 2048 63 us, with
 // four waves 72; 256 tokens: two tiles 83, one 94).
-constexpr int64_t kStreamRows = 64;
+constexpr int64_t kStreamRows = 64, kStreamExpertRows = 32;
 template <bool BROWS>
 static int stream_by_rows(const F8Params& p, int64_t rows, hipStream_t s)
 {
@@ -145,19 +156,126 @@ static int stream_by_rows(const F8Params& p, int64_t rows, hipStream_t s)
     return panels < 512 ? launch_stream<4, 1, 2, 4, BROWS>(p, s) : launch_stream<4, 4, 1, 4, BROWS>(p, s);
 }
 
-static int launch_gemm(F8Params p, hipStream_t s)
+// Tiles for more rows.
+enum Tile { kTile256, kTile128x256, kTile128, kTile128Deep, kTile64, kTile32, kTiles };
+struct TileForm {
+    int bm, bn;
+    int resident;                                      // workgroups on a compute unit
+    float chunk_us[4];                                 // a round of them takes for a chunk: [2 exact + rows of B]
+};
+
+// Measured (MI355X, 8192 x 8192 x 8192; 1024 and 512 rows of 4096 to 8192 for the
+// deep and the small tiles): 256 x 256 has 474 us, 128 x 256 573, 128 x 128 620,
+// 64 x 64 1,015; with a scale for each row of B, 710 (registers spill), 686, 705,
+// 1,148; exact 1,603, 984, 1,002, 1,502.
+constexpr float kNever = 1e9f;
+static const TileForm kForms[kTiles] = {{256, 256, 1, {1.85f, kNever, kNever, kNever}},
+                                        {128, 256, 1, {1.13f, 1.36f, 1.95f, 2.10f}},
+                                        {128, 128, 2, {1.21f, 1.38f, 1.96f, 2.13f}},
+                                        {128, 128, 1, {0.80f, 0.85f, 1.20f, 1.32f}},
+                                        {64, 64, 2, {0.52f, 0.60f, 0.80f, 0.88f}},
+                                        {32, 64, 3, {0.46f, 0.50f, 0.60f, 0.66f}}};
+
+struct TilePlan {
+    Tile tile;
+    int split, each;
+};
+
+// The tile, and into how many parts the reduction is split, with the smallest
+// estimate: rounds of workgroups on the compute units times the time of their
+// chunks, 3 us a round for its beginning and end, and for parts a second launch
+// that adds up their slabs.  Without parts 100 x 1000 x 16384 takes 45 us, 32
+// workgroups of 128 chunks.
+static TilePlan plan_tiles(int64_t M, int64_t N, int chunks, int64_t experts, int form)
+{
+    TilePlan best{kTile128, 1, chunks};
+    double least = 1e30;
+    const double cus = (double)compute_units();
+    for (int t = 0; t < kTiles; ++t) {
+        const TileForm& f = kForms[t];
+        // an expert's last tile is half full
+        const double tiles_m = experts ? (double)M / f.bm + 0.5 * (double)experts : (double)ceil_div(M, f.bm);
+        const double tiles = std::ceil(tiles_m) * (double)ceil_div(N, f.bn);
+        for (int split = 1; split <= (experts ? 1 : 16); split *= 2) {
+            const int each = (int)ceil_div(chunks, split);
+            if (split > 1 && (each < 4 || ceil_div(chunks, each) != split))
+                break;
+            const double rounds = std::ceil(tiles * split / (cus * f.resident));
+            double us = rounds * (each * (double)f.chunk_us[form] + 3.0);
+            if (split > 1)
+                us += 3.0 + (double)M * (double)N * (8.0 * split + 4.0) / 4e6;
+            if (us < least) {
+                least = us;
+                best = {(Tile)t, split, each};
+            }
+        }
+    }
+    return best;
+}
+
+static size_t slabs_bytes(const TilePlan& t, int64_t M, int64_t N)
+{
+    return t.split > 1 ? (size_t)t.split * (size_t)splitk_slab(M, N) * 4 : 0;
+}
+
+template <bool BROWS, bool EXACT>
+static int launch_tile(const F8Params& p, Tile tile, hipStream_t s)
+{
+    // eight waves where the sums and fragments of a chunk fit their registers
+    constexpr int WGN = BROWS || EXACT ? 2 : 4;
+    switch (tile) {
+    case kTile256:
+        if constexpr (!BROWS && !EXACT)
+            return launch_tiles<256, 256, 2, 4, 2, BROWS, EXACT>(p, s);
+        [[fallthrough]];
+    case kTile128x256:
+        return launch_tiles<128, 256, 2, 4, 3, BROWS, EXACT>(p, s);
+    case kTile128:
+        return launch_tiles<128, 128, 2, WGN, 2, BROWS, EXACT>(p, s);
+    case kTile128Deep:
+        return launch_tiles<128, 128, 2, 4, 4, BROWS, EXACT>(p, s);
+    case kTile64:
+        return launch_tiles<64, 64, 2, 2, 4, BROWS, EXACT>(p, s);
+    default:
+        return launch_tiles<32, 64, 1, 4, 4, BROWS, EXACT>(p, s);
+    }
+}
+
+// Rows that a workgroup of the streaming kernel would have.
+static int64_t stream_rows(int64_t M, int64_t experts)
+{
+    return experts ? ceil_div(M, std::min(experts, M)) : M;
+}
+
+static int launch_gemm(F8Params p, void* workspace, size_t workspace_bytes, hipStream_t s)
 {
     p.group_m = 8;
     p.vec_out = p.N % 4 == 0 && (uintptr_t)p.C % (p.out_bf16 ? 8 : 16) == 0;
-    // rows that a workgroup of the streaming kernel would have
-    const int64_t rows = p.offsets ? ceil_div(p.M, std::min<int64_t>(p.E, p.M)) : p.M;
-    if (rows <= kStreamRows)
-        return p.b_rows == 1 ? stream_by_rows<true>(p, rows, s) : stream_by_rows<false>(p, rows, s);
-    if (p.out_bf16)
-        return p.b_rows == 1 ? launch_tiles<256, 256, 2, 4, true, false>(p, s)
-                             : launch_tiles<256, 256, 2, 4, false, false>(p, s);
-    return p.b_rows == 1 ? launch_tiles<128, 128, 2, 2, true, true>(p, s)
-                         : launch_tiles<128, 128, 2, 2, false, true>(p, s);
+    const bool by_rows = p.b_rows == 1, exact = !p.out_bf16;
+    const int64_t experts = p.offsets ? std::min<int64_t>(p.E, p.M) : 0, rows = stream_rows(p.M, experts);
+    if (rows <= (experts ? kStreamExpertRows : kStreamRows))
+        return by_rows ? stream_by_rows<true>(p, rows, s) : stream_by_rows<false>(p, rows, s);
+    const TilePlan t = plan_tiles(p.M, p.N, p.chunks, experts, 2 * exact + by_rows);
+    const F8Params whole = p;
+    p.split = t.split;
+    p.each = t.each;
+    if (t.split > 1) {
+        if (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < slabs_bytes(t, p.M, p.N))
+            return set_error(TG_E_INVAL,
+                             "the workspace must be 16-byte aligned and hold tg_gemm_fp8_workspace_bytes() bytes");
+        p.slabs = static_cast<float*>(workspace);
+        p.slab = splitk_slab(p.M, p.N);
+        p.bias = nullptr;
+        p.act = 0;
+        p.out_bf16 = 0;
+        p.vec_out = p.N % 4 == 0;
+    }
+    const int st = exact ? by_rows ? launch_tile<true, true>(p, t.tile, s) : launch_tile<false, true>(p, t.tile, s)
+                         : by_rows ? launch_tile<true, false>(p, t.tile, s) : launch_tile<false, false>(p, t.tile, s);
+    if (st != TG_OK || t.split == 1)
+        return st;
+    const hipError_t e = splitk_reduce(p.slabs, t.split, whole.M, whole.N, whole.bias, whole.C, whole.out_bf16, whole.act, s);
+    return e == hipSuccess ? TG_OK : set_hip_error(e, "gemm_fp8 sums launch");
 }
 
 static int check_product(int64_t M, int64_t N, int64_t K, int dtype)
@@ -205,13 +323,15 @@ int tg_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes)
     if (!bytes || M < 0 || N < 0 || K < 1 || M > kMaxSide || N > kMaxSide || K > kMaxDepth)
         return set_error(TG_E_INVAL, "bad size, or bytes is NULL");
     *bytes = 0;
+    if (M > kStreamRows && N > 0)
+        for (int form = 0; form < 4; ++form)
+            *bytes = std::max(*bytes, slabs_bytes(plan_tiles(M, N, (int)ceil_div(K, 128), 0, form), M, N));
     return TG_OK;
 }
 
 int tg_gemm_fp8(int64_t M, int64_t N, int64_t K, const tg_f8* A, const tg_f8* B, const float* bias, void* C,
                 int dtype, int act, void* workspace, size_t workspace_bytes)
 {
-    (void)workspace, (void)workspace_bytes;
     int st = check_product(M, N, K, dtype);
     if (st != TG_OK)
         return st;
@@ -229,7 +349,7 @@ int tg_gemm_fp8(int64_t M, int64_t N, int64_t K, const tg_f8* A, const tg_f8* B,
     F8Params p = params_of(M, N, K, *A, *B, C, dtype);
     p.bias = bias;
     p.act = act;
-    return launch_gemm(p, current_stream());
+    return launch_gemm(p, workspace, workspace_bytes, current_stream());
 }
 
 int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8* A, const tg_f8* B,
@@ -254,7 +374,7 @@ int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8* 
     F8Params p = params_of(rows, N, K, *A, *B, C, dtype);
     p.offsets = offsets;
     p.E = (int)E;
-    return launch_gemm(p, current_stream());
+    return launch_gemm(p, nullptr, 0, current_stream());
 }
 
 }  // extern "C"
