@@ -33,6 +33,7 @@ struct F8Params {
     int b_rows;                                        // rows of B that share a scale, 1 or 128
     int out_bf16, act;
     int vec_out;                                       // four results of a row are one aligned access
+    int line_out;                                      // and eight bf16
     int group_m;                                       // row tiles that go through the column tiles together
     int split, each;                                   // parts of the reduction, chunks of one
     float* slabs;                                      // their sums, `slab` floats apart
@@ -161,20 +162,21 @@ enum Tile { kTile256, kTile128x256, kTile128, kTile128Deep, kTile64, kTile32, kT
 struct TileForm {
     int bm, bn;
     int resident;                                      // workgroups on a compute unit
-    float chunk_us[4];                                 // a round of them takes for a chunk: [2 exact + rows of B]
+    float round_us;                                    // beginning and end of a round of them
+    float chunk_us[4];                                 // a chunk of a round: [2 exact + rows of B]
 };
 
-// Measured (MI355X, 8192 x 8192 x 8192; 1024 and 512 rows of 4096 to 8192 for the
-// deep and the small tiles): 256 x 256 has 474 us, 128 x 256 573, 128 x 128 620,
-// 64 x 64 1,015; with a scale for each row of B, 710 (registers spill), 686, 705,
-// 1,148; exact 1,603, 984, 1,002, 1,502.
+// Measured (MI355X, 8192 x 8192 by 8192 and by 1024; the deep and the small tiles
+// with 512 and 100 rows): 8192 deep, 256 x 256 has 454 us, 128 x 256 554, 128 x 128
+// 622, 64 x 64 994; with a scale for each row of B 708 (its registers do not
+// suffice), 660, 705, 1,106; exact 1,531, 937, 1,002, 1,425.
 constexpr float kNever = 1e9f;
-static const TileForm kForms[kTiles] = {{256, 256, 1, {1.85f, kNever, kNever, kNever}},
-                                        {128, 256, 1, {1.13f, 1.36f, 1.95f, 2.10f}},
-                                        {128, 128, 2, {1.21f, 1.38f, 1.96f, 2.13f}},
-                                        {128, 128, 1, {0.80f, 0.85f, 1.20f, 1.32f}},
-                                        {64, 64, 2, {0.52f, 0.60f, 0.80f, 0.88f}},
-                                        {32, 64, 3, {0.46f, 0.50f, 0.60f, 0.66f}}};
+static const TileForm kForms[kTiles] = {{256, 256, 1, 8.7f, {1.64f, kNever, kNever, kNever}},
+                                        {128, 256, 1, 5.3f, {1.00f, 1.21f, 1.68f, 1.85f}},
+                                        {128, 128, 2, 4.3f, {1.15f, 1.30f, 1.85f, 2.00f}},
+                                        {128, 128, 1, 4.0f, {0.75f, 0.80f, 1.10f, 1.20f}},
+                                        {64, 64, 2, 2.5f, {0.45f, 0.50f, 0.64f, 0.72f}},
+                                        {32, 64, 3, 2.0f, {0.42f, 0.46f, 0.52f, 0.58f}}};
 
 struct TilePlan {
     Tile tile;
@@ -182,9 +184,8 @@ struct TilePlan {
 };
 
 // The tile, and into how many parts the reduction is split, with the smallest
-// estimate: rounds of workgroups on the compute units times the time of their
-// chunks, 3 us a round for its beginning and end, and for parts a second launch
-// that adds up their slabs.  Without parts 100 x 1000 x 16384 takes 45 us, 32
+// estimate: rounds of workgroups on the compute units times what they take, and
+// for parts a second launch that adds up their slabs.  Without parts 100 x 1000 x 16384 takes 45 us, 32
 // workgroups of 128 chunks.
 static TilePlan plan_tiles(int64_t M, int64_t N, int chunks, int64_t experts, int form)
 {
@@ -201,7 +202,7 @@ static TilePlan plan_tiles(int64_t M, int64_t N, int chunks, int64_t experts, in
             if (split > 1 && (each < 4 || ceil_div(chunks, each) != split))
                 break;
             const double rounds = std::ceil(tiles * split / (cus * f.resident));
-            double us = rounds * (each * (double)f.chunk_us[form] + 3.0);
+            double us = rounds * (each * (double)f.chunk_us[form] + (double)f.round_us);
             if (split > 1)
                 us += 3.0 + (double)M * (double)N * (8.0 * split + 4.0) / 4e6;
             if (us < least) {
@@ -251,6 +252,7 @@ static int launch_gemm(F8Params p, void* workspace, size_t workspace_bytes, hipS
 {
     p.group_m = 8;
     p.vec_out = p.N % 4 == 0 && (uintptr_t)p.C % (p.out_bf16 ? 8 : 16) == 0;
+    p.line_out = p.N % 8 == 0 && (uintptr_t)p.C % 16 == 0;
     const bool by_rows = p.b_rows == 1, exact = !p.out_bf16;
     const int64_t experts = p.offsets ? std::min<int64_t>(p.E, p.M) : 0, rows = stream_rows(p.M, experts);
     if (rows <= (experts ? kStreamExpertRows : kStreamRows))

@@ -15,12 +15,8 @@
 namespace tg {
 
 // Four neighbouring results of a row.
-__device__ __forceinline__ void store_results(const F8Params& p, int64_t row, int64_t col, const f32x4_t& sums)
+__device__ __forceinline__ void store_results(const F8Params& p, int64_t row, int64_t col, const f32x4_t& v)
 {
-    float v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        v[e] = apply_act(sums[e] + (p.bias && col + e < p.N ? p.bias[col + e] : 0.0f), p.act);
     const int64_t at = row * p.N + col;
     if (p.out_bf16) {
         unsigned short* to = static_cast<unsigned short*>(p.C) + at;
@@ -183,8 +179,12 @@ __device__ __forceinline__ void f8_stream(const F8Params& p, char* lds, int64_t 
             sum += sums[w * P * MT * 64 + t];
         const int j = t / (MT * 64), i = t / 64 % MT, l = t % 64;
         const int64_t row = m0 + 16 * i + l % 16, col = n0 + 16 * j + l / 16 * 4;
-        if (row < m1 && col < p.N)
+        if (row < m1 && col < p.N) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum[e] = apply_act(sum[e] + (p.bias && col + e < p.N ? p.bias[col + e] : 0.0f), p.act);
             store_results(p, row, col, sum);
+        }
     }
 }
 

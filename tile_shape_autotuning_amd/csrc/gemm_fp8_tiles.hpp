@@ -151,26 +151,26 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, char* lds, int64_t m0
     auto row_of = [](int x) { return x < TAIL ? x / FN : FM - 2 + ((x - TAIL) & 1); };
     auto col_of = [](int x) { return x < TAIL ? x % FN : (x - TAIL) / 2; };
 
+    load_scales(0);
 #pragma unroll
     for (int t = 0; t < ST; ++t) {
         const Source s = source(t, t);
 #pragma unroll
         for (int q = 0; q < Cf::INST; ++q)
             fetch(s, q);
-        if (t == 0) {
-            load_scales(0);
-            keep_scales(0);
-        }
     }
+    keep_scales(0);
     wait_vmcnt<(ST - 1) * Cf::INST>();
     wait_lgkm0();
     block_barrier();
     Base cur = base_of(0);
+    // in the order in which a chunk reads the next one's: the first product then
+    // waits for its own fragments only
+    read_a(cur, 0);
+    read_a(cur, 1);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
         read_b(cur, j);
-    read_a(cur, 0);
-    read_a(cur, 1);
 
     int buf = 0;
     for (int c = 0; c < chunks; ++c) {
@@ -183,21 +183,19 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, char* lds, int64_t m0
         const Base nxt = base_of(nbuf);
         const Source src = source(c + ST, buf);
 
-        float sa[FM];
+        float sa[FM], s = 1.0f;
         f32x4_t sb[FN];
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-            sa[i] = sc[wm * Cf::WM + 16 * i + l16];
         if constexpr (BROWS) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 sb[j] = *reinterpret_cast<const f32x4_t*>(sc + BM + wn * Cf::WN + 16 * j + 4 * g);
         } else {
-            const float s = sc[BM + wn * Cf::WN / 128];
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                sa[i] *= s;
+            s = sc[BM + wn * Cf::WN / 128];
         }
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            sa[i] = sc[wm * Cf::WM + 16 * i + l16];
+        __builtin_amdgcn_sched_barrier(0);             // on their way before the first product, not waited for
         Expanded be[EXACT ? FN : 1], ae[EXACT ? 2 : 1];
         if constexpr (EXACT) {
 #pragma unroll
@@ -207,6 +205,8 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, char* lds, int64_t m0
         f32x4_t d[DR];
         auto add = [&](int x) {
             const int i = row_of(x), j = col_of(x);
+            if (!BROWS && j == 0)
+                sa[i] *= s;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 acc[i][j][r] = fmaf(d[x % DR][r], BROWS ? sa[i] * sb[j][r] : sa[i], acc[i][j][r]);
@@ -259,8 +259,73 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, char* lds, int64_t m0
     }
     wait_vm_all();                                     // transfers still on their way to LDS
 
+    f32x4_t bias[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int col = wn * Cf::WN + 16 * j + 4 * g + e;
+            bias[j][e] = p.bias && col < cols ? p.bias[n0 + col] : 0.0f;
+        }
+    // a row of results at a time: more would not fit the registers
+    auto finish = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] += bias[j];
+        if (p.act == TG_ACT_RELU) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = apply_act(acc[i][j][e], TG_ACT_RELU);
+        } else if (p.act == TG_ACT_GELU) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = apply_act(acc[i][j][e], TG_ACT_GELU);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (Cf::WN % 64 == 0 && !EXACT) {
+        if (p.out_bf16 && p.line_out) {
+            // whole lines of bf16 through the wave's own part of the ring: eight
+            // columns, 16 bytes, of row r at unit u ^ (r & 7) of each 128 bytes
+            block_barrier();                           // every wave's transfers and reads are done
+            constexpr int ROW = Cf::WN * 2, UNITS = ROW / 16, RPI = 64 / UNITS;
+            static_assert(Cf::W * Cf::WM * ROW <= ST * Cf::STAGE && Cf::WM % RPI == 0, "the tile fits the ring");
+            char* const mine = lds + wave * Cf::WM * ROW;
+            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                finish(i);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const int r = 16 * i + l16, u = 2 * j + (g >> 1);
+                    const f32x4_t v = acc[i][j];
+                    *reinterpret_cast<u32x2*>(mine + r * ROW + (u ^ (l16 & 7)) * 16 + (g & 1) * 8) =
+                        u32x2{f32_to_bf16_rne(v[0]) | (unsigned)f32_to_bf16_rne(v[1]) << 16,
+                              f32_to_bf16_rne(v[2]) | (unsigned)f32_to_bf16_rne(v[3]) << 16};
+                }
+            }
+            wait_lgkm0();
+            __asm__ __volatile__("" ::: "memory");
+            // RPI rows an instruction
+            const int u = lane % UNITS, col = wn * Cf::WN + 8 * u;
+            unsigned short* const to = static_cast<unsigned short*>(p.C) + (m0 + wm * Cf::WM) * p.N + n0 + col;
+#pragma unroll 4
+            for (int q = 0; q < Cf::WM / RPI; ++q) {
+                const int r = q * RPI + lane / UNITS;
+                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + r * ROW + (u ^ (r & 7)) * 16);
+                if (wm * Cf::WM + r < rows && col < cols)
+                    *reinterpret_cast<u32x4_t*>(to + (int64_t)r * p.N) = v;
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
+        finish(i);
         const int r = wm * Cf::WM + 16 * i + l16;
         if (r >= rows)
             continue;

@@ -16,6 +16,8 @@ constexpr int kOrderExperts = 1024, kOrderChoices = 16;
 constexpr int64_t kUnits = (int64_t)1 << 31;           // pieces of all rows of a call
 constexpr int64_t kOrderTokens = (int64_t)1 << 24, kOrderWidth = (int64_t)1 << 24;
 
+static unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 20); }
+
 // ---------------------------------------------------------------- sort
 // Few pairs: a workgroup takes one expert, counts the pairs of the experts before
 // it, then walks the pairs in order and numbers its own.  The last workgroup
@@ -430,26 +432,129 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(CombineParams p)
     }
 }
 
-template <bool BF16>
-static void launch_combine(const CombineParams& p, unsigned grid, hipStream_t s)
+// Rows of up to 1 KiB: sixteen lanes take a token, lane j of them has its j-th
+// row, and the four tokens of a wave go their own ways.
+constexpr int64_t kNarrow = 1024;
+
+template <int KM>
+struct TeamRows {
+    int r[KM];
+    float w[KM];
+    __device__ __forceinline__ TeamRows(const CombineParams& p, int64_t t, int lane)
+    {
+        const int l = lane & 15;
+        const bool has = t < p.T && l < p.k;
+        const int at = has ? p.position[t * p.k + l] : -1;
+        const float wl = has && p.weights ? p.weights[t * p.k + l] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {                 // every lane runs here
+            const int v = __shfl(at, (lane & 48) | j);
+            r[j] = v < p.rows ? v : -1;
+            w[j] = __shfl(wl, (lane & 48) | j);
+        }
+    }
+};
+
+template <bool BF16, int KM>
+__global__ void __launch_bounds__(256) moe_combine_narrow_kernel(CombineParams p)
 {
-    if (p.k <= 4)
-        hipLaunchKernelGGL((moe_combine_kernel<BF16, 4>), dim3(grid), dim3(256), 0, s, p);
-    else if (p.k <= 8)
-        hipLaunchKernelGGL((moe_combine_kernel<BF16, 8>), dim3(grid), dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((moe_combine_kernel<BF16, 16>), dim3(grid), dim3(256), 0, s, p);
+    using S = Slice<BF16>;
+    const int lane = threadIdx.x & 63;
+    for (int64_t t0 = (int64_t)blockIdx.x * 16; t0 < p.T; t0 += (int64_t)gridDim.x * 16) {
+        const int64_t t = t0 + (threadIdx.x >> 4);
+        const TeamRows<KM> rows(p, t, lane);
+        for (int64_t h0 = 0; h0 < p.H; h0 += 16 * S::N) {
+            const int64_t h = h0 + (lane & 15) * S::N;
+            S x[KM], y;
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (rows.r[j] >= 0)
+                    x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+#pragma unroll
+            for (int i = 0; i < S::N; ++i)
+                y.v[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (rows.r[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < S::N; ++i)
+                        y.v[i] = fmaf(rows.w[j], x[j].v[i], y.v[i]);
+            if (t < p.T)
+                y.store(row_at<BF16>(p.y, t, p.H), h, p.H);
+        }
+    }
 }
 
+template <bool BF16, int KM>
+__global__ void __launch_bounds__(256) moe_combine_grad_narrow_kernel(CombineParams p)
+{
+    using S = Slice<BF16>;
+    const int lane = threadIdx.x & 63;
+    for (int64_t t0 = (int64_t)blockIdx.x * 16; t0 < p.T; t0 += (int64_t)gridDim.x * 16) {
+        const int64_t t = t0 + (threadIdx.x >> 4);
+        const TeamRows<KM> rows(p, t, lane);
+        float dot[KM] = {};
+        for (int64_t h0 = 0; h0 < p.H; h0 += 16 * S::N) {
+            const int64_t h = t < p.T ? h0 + (lane & 15) * S::N : p.H;
+            S dy, x[KM];
+            dy.load(row_at<BF16>(p.dy, t < p.T ? t : 0, p.H), h, p.H);
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (rows.r[j] >= 0)
+                    x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (rows.r[j] >= 0) {
+                    S d;
+#pragma unroll
+                    for (int i = 0; i < S::N; ++i) {
+                        dot[j] = fmaf(dy.v[i], x[j].v[i], dot[j]);
+                        d.v[i] = rows.w[j] * dy.v[i];
+                    }
+                    d.store(row_at<BF16>(p.dx, rows.r[j], p.H), h, p.H);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {                 // every lane runs here
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1)
+                dot[j] += __shfl_xor(dot[j], off);
+            if (t < p.T && (lane & 15) == j && j < p.k)
+                p.dweights[t * p.k + j] = dot[j];
+        }
+    }
+}
+
+template <bool BF16, int KM>
+static void launch_combine(const CombineParams& p, hipStream_t s)
+{
+    if (p.H * (BF16 ? 2 : 4) <= kNarrow)
+        hipLaunchKernelGGL((moe_combine_narrow_kernel<BF16, KM>), dim3(grid_of(ceil_div(p.T, 16))), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, KM>), dim3(grid_of(ceil_div(p.T * p.pieces, 4))), dim3(256), 0, s,
+                           p);
+}
+
+template <bool BF16, int KM>
+static void launch_combine_grad(const CombineParams& p, hipStream_t s)
+{
+    if (p.H * (BF16 ? 2 : 4) <= kNarrow)
+        hipLaunchKernelGGL((moe_combine_grad_narrow_kernel<BF16, KM>), dim3(grid_of(ceil_div(p.T, 16))), dim3(256), 0, s,
+                           p);
+    else
+        hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, KM>), dim3(grid_of(p.T)), dim3(256), 0, s, p);
+}
+
+// Up to 4, 8 or 16 rows of a token in registers.
 template <bool BF16>
-static void launch_combine_grad(const CombineParams& p, unsigned grid, hipStream_t s)
+static void by_choices(const CombineParams& p, bool grad, hipStream_t s)
 {
     if (p.k <= 4)
-        hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, 4>), dim3(grid), dim3(256), 0, s, p);
+        grad ? launch_combine_grad<BF16, 4>(p, s) : launch_combine<BF16, 4>(p, s);
     else if (p.k <= 8)
-        hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, 8>), dim3(grid), dim3(256), 0, s, p);
+        grad ? launch_combine_grad<BF16, 8>(p, s) : launch_combine<BF16, 8>(p, s);
     else
-        hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, 16>), dim3(grid), dim3(256), 0, s, p);
+        grad ? launch_combine_grad<BF16, 16>(p, s) : launch_combine<BF16, 16>(p, s);
 }
 
 // ---------------------------------------------------------------- checks
@@ -501,8 +606,6 @@ static int check_combine(int64_t T, int k, int64_t rows, int64_t H, int dtype, c
         return set_error(TG_E_INVAL, "rows are fp32 or bf16");
     return TG_OK;
 }
-
-static unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 20); }
 
 }  // namespace tg
 
@@ -592,8 +695,7 @@ int tg_moe_combine(int64_t T, int k, int64_t rows, int64_t H, const void* x, int
                           (int)ceil_div(H, dtype == TG_BF16 ? 512 : 256)};
     if (T * p.pieces > kUnits)
         return set_error(TG_E_UNSUPPORTED, "moe_combine: more than 2^31 pieces of 1 KiB");
-    const unsigned grid = grid_of(ceil_div(T * p.pieces, 4));
-    dtype == TG_BF16 ? launch_combine<true>(p, grid, current_stream()) : launch_combine<false>(p, grid, current_stream());
+    dtype == TG_BF16 ? by_choices<true>(p, false, current_stream()) : by_choices<false>(p, false, current_stream());
     return launched("moe_combine launch");
 }
 
@@ -610,8 +712,7 @@ int tg_moe_combine_grad(int64_t T, int k, int64_t rows, int64_t H, const void* d
     if (!have_device())
         return set_error(TG_E_UNSUPPORTED, "no HIP device");
     const CombineParams p{x, dy, position, weights, nullptr, dx, dweights, T, rows, H, k, 0};
-    dtype == TG_BF16 ? launch_combine_grad<true>(p, grid_of(T), current_stream())
-                     : launch_combine_grad<false>(p, grid_of(T), current_stream());
+    dtype == TG_BF16 ? by_choices<true>(p, true, current_stream()) : by_choices<false>(p, true, current_stream());
     return launched("moe_combine_grad launch");
 }
 
