@@ -147,31 +147,31 @@ __device__ __forceinline__ unsigned resolve4(const float* x, const Scale& s, uns
     return c;
 }
 
+__device__ __forceinline__ unsigned encode4(const float* x, const Scale& s)
+{
+    float lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // above 448 only where a subnormal scale was rounded down
+        float q = x[i] * s.inv;
+        if (s.by != 1.0f)
+            q = __builtin_amdgcn_fmed3f((x[i] * s.by) * s.inv, -448.0f, 448.0f);
+        lo[i] = q * (1.0f - 0x1p-22f);
+        hi[i] = q * (1.0f + 0x1p-22f);
+    }
+    const int a = __builtin_amdgcn_cvt_pk_fp8_f32(lo[2], lo[3], __builtin_amdgcn_cvt_pk_fp8_f32(lo[0], lo[1], 0, false), true);
+    const int b = __builtin_amdgcn_cvt_pk_fp8_f32(hi[2], hi[3], __builtin_amdgcn_cvt_pk_fp8_f32(hi[0], hi[1], 0, false), true);
+    unsigned out = (unsigned)a;
+    if (a != b)
+        out = resolve4(x, s, (unsigned)a, (unsigned)b);
+    if (!(s.s > 0.0f))
+        out = s.s == 0.0f ? 0u : 0x7F7F7F7Fu;
+    return out;
+}
+
 __device__ __forceinline__ u32x2_t8 encode8(const float (&v)[8], const Scale& s)
 {
-    u32x2_t8 out;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float lo[4], hi[4];
-        const float* x = v + 4 * h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // above 448 only where a subnormal scale was rounded down
-            float q = x[i] * s.inv;
-            if (s.by != 1.0f)
-                q = __builtin_amdgcn_fmed3f((x[i] * s.by) * s.inv, -448.0f, 448.0f);
-            lo[i] = q * (1.0f - 0x1p-22f);
-            hi[i] = q * (1.0f + 0x1p-22f);
-        }
-        const int a = __builtin_amdgcn_cvt_pk_fp8_f32(lo[2], lo[3], __builtin_amdgcn_cvt_pk_fp8_f32(lo[0], lo[1], 0, false), true);
-        const int b = __builtin_amdgcn_cvt_pk_fp8_f32(hi[2], hi[3], __builtin_amdgcn_cvt_pk_fp8_f32(hi[0], hi[1], 0, false), true);
-        out[h] = (unsigned)a;
-        if (a != b)
-            out[h] = resolve4(x, s, (unsigned)a, (unsigned)b);
-        if (!(s.s > 0.0f))
-            out[h] = s.s == 0.0f ? 0u : 0x7F7F7F7Fu;
-    }
-    return out;
+    return u32x2_t8{encode4(v, s), encode4(v + 4, s)};
 }
 
 // Codes from element n on are zero.
@@ -184,15 +184,12 @@ __device__ __forceinline__ u32x2_t8 first_of(u32x2_t8 c, int n)
     return c;
 }
 
-__device__ __forceinline__ void decode8(u32x2_t8 c, const Scale& s, float (&v)[8])
+__device__ __forceinline__ void decode4(unsigned c, const Scale& s, float* v)
 {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        v[4 * h] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 0) * s.s;
-        v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 1) * s.s;
-        v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 2) * s.s;
-        v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[h], 3) * s.s;
-    }
+    v[0] = __builtin_amdgcn_cvt_f32_fp8((int)c, 0) * s.s;
+    v[1] = __builtin_amdgcn_cvt_f32_fp8((int)c, 1) * s.s;
+    v[2] = __builtin_amdgcn_cvt_f32_fp8((int)c, 2) * s.s;
+    v[3] = __builtin_amdgcn_cvt_f32_fp8((int)c, 3) * s.s;
 }
 
 // x [R][K].  Sixteen lanes take a chunk of a row.  BLOCK = 1: U of them, each on
@@ -262,7 +259,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_along_kernel(F8QuantParams p
                 const u32x2_t8 c = first_of(encode8(v[u], s), n);
                 *reinterpret_cast<u32x2_t8*>(p.codes + row[u] * Kp + k) = c;
                 if (p.values) {
-                    decode8(c, s, v[u]);
+                    decode4(c[0], s, v[u]);
+                    decode4(c[1], s, v[u] + 4);
                     store8<BF16>(p.values, row[u] * p.K + k, n, v[u]);
                 }
                 if (BLOCK == 1 && l16 == 0)
@@ -274,50 +272,61 @@ __global__ void __launch_bounds__(256) fp8_quantize_along_kernel(F8QuantParams p
     }
 }
 
-// x [K][R]: a workgroup takes 128 k of 128 rows, a thread eight neighbouring rows
-// of k = 64 h + 4 (tid / 16) + i, h = 0, 1, i = 0..3.
+// x [K][R]: a workgroup takes 128 k of ROWS rows, a thread eight neighbouring rows
+// of four neighbouring k.  64 rows where they need no common scale: 32 elements a
+// thread and four workgroups a compute unit (4096 x 8192 bf16 with values 49 us;
+// 128 rows of eight k a thread leave two, which load, compute and store one after
+// the other, 75 us; workgroups numbered along k instead of the rows 70).
 template <bool BF16, int BLOCK>
-__global__ void __launch_bounds__(256) fp8_quantize_across_kernel(F8QuantParams p)
+struct Across {
+    static constexpr int ROWS = BLOCK == 1 ? 64 : 128;
+    static constexpr int LANES = ROWS / 8;             // side by side along the rows
+    static constexpr int THREADS = LANES * 32, WAVES = THREADS / 64;
+};
+
+template <bool BF16, int BLOCK>
+__global__ void __launch_bounds__((Across<BF16, BLOCK>::THREADS), 4) fp8_quantize_across_kernel(F8QuantParams p)
 {
-    constexpr int PITCH = 33;                          // dwords of a row of codes: threads 16 apart on other banks
-    __shared__ unsigned out[128 * PITCH];
-    __shared__ unsigned tops[BLOCK == 1 ? 4 * 128 : 4];
-    const int l16 = threadIdx.x & 15, team = threadIdx.x >> 4, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t Kp = (int64_t)p.chunks * 128, blocks = (p.R + 127) / 128;
+    using Cf = Across<BF16, BLOCK>;
+    constexpr int ROWS = Cf::ROWS, LANES = Cf::LANES, PITCH = 33;   // dwords of a row of codes: other banks for the next
+    __shared__ unsigned out[ROWS * PITCH];
+    __shared__ unsigned tops[BLOCK == 1 ? Cf::WAVES * ROWS : Cf::WAVES];
+    const int rl = threadIdx.x % LANES, team = threadIdx.x / LANES, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t Kp = (int64_t)p.chunks * 128, groups = (p.R + ROWS - 1) / ROWS;
     for (int64_t work = blockIdx.x; work < p.works; work += gridDim.x) {
-        // neighbouring workgroups read neighbouring rows' parts of the same lines' pages
-        const int64_t mat = work / (blocks * p.chunks), in = work - mat * blocks * p.chunks;
-        const int64_t chunk = in / blocks, rb = in - chunk * blocks;
-        const int64_t r0 = rb * 128 + 8 * l16, k0 = chunk * 128 + 4 * team, base = mat * p.R * p.K;
+        // neighbouring workgroups have neighbouring rows of the same k
+        const int64_t mat = work / (groups * p.chunks), in = work - mat * groups * p.chunks;
+        const int64_t chunk = in / groups, rb = in - chunk * groups;
+        const int64_t r0 = rb * ROWS + 8 * rl, k0 = chunk * 128 + 4 * team, base = mat * p.R * p.K;
         const int n = (int)max((int64_t)0, min((int64_t)8, p.R - r0));
-        float v[8][8];                                 // [h, i][row]
+        const int left = (int)max((int64_t)0, min((int64_t)4, p.K - k0));
+        float v[4][8];                                 // [k][row]
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int64_t k = k0 + 64 * (q >> 2) + (q & 3);
-            load8<BF16>(p.x, base + k * p.R + r0, k < p.K ? n : 0, v[q]);
-        }
+        for (int q = 0; q < 4; ++q)
+            load8<BF16>(p.x, base + (k0 + q) * p.R + r0, q < left ? n : 0, v[q]);
         unsigned top[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             top[e] = 0;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
+            for (int q = 0; q < 4; ++q)
                 top[e] = max(top[e], __float_as_uint(v[q][e]) & 0x7FFFFFFFu);
-            top[e] = max(top[e], (unsigned)__shfl_xor((int)top[e], 16));
-            top[e] = max(top[e], (unsigned)__shfl_xor((int)top[e], 32));
+#pragma unroll
+            for (int off = LANES; off < 64; off <<= 1)
+                top[e] = max(top[e], (unsigned)__shfl_xor((int)top[e], off));
         }
         __syncthreads();                               // the last work's codes and tops are read
         if constexpr (BLOCK == 1) {
-            if (lane < 16)
+            if (lane < LANES)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    tops[wave * 128 + 8 * l16 + e] = top[e];
+                    tops[wave * ROWS + 8 * rl + e] = top[e];
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int r = 8 * l16 + e;
-                top[e] = max(max(tops[r], tops[128 + r]), max(tops[256 + r], tops[384 + r]));
-            }
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int w = 0; w < Cf::WAVES; ++w)
+                    top[e] = max(top[e], tops[w * ROWS + 8 * rl + e]);
         } else {
             unsigned t = top[0];
 #pragma unroll
@@ -327,7 +336,9 @@ __global__ void __launch_bounds__(256) fp8_quantize_across_kernel(F8QuantParams 
             if (lane == 0)
                 tops[wave] = t;
             __syncthreads();
-            t = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+#pragma unroll
+            for (int w = 0; w < Cf::WAVES; ++w)
+                t = max(t, tops[w]);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 top[e] = t;
@@ -335,43 +346,36 @@ __global__ void __launch_bounds__(256) fp8_quantize_across_kernel(F8QuantParams 
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const Scale s(top[e]);
-            float x[8];
+            float x[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
+            for (int q = 0; q < 4; ++q)
                 x[q] = v[q][e];
-            u32x2_t8 c = encode8(x, s);
-            // k past K
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t left = p.K - (k0 + 64 * h);
-                c[h] = left <= 0 ? 0u : left < 4 ? c[h] & ((1u << (8 * (int)left)) - 1) : c[h];
-                out[(8 * l16 + e) * PITCH + 16 * h + team] = c[h];
-            }
+            unsigned c = encode4(x, s);
+            c = left <= 0 ? 0u : left < 4 ? c & ((1u << (8 * left)) - 1) : c;      // k past K
+            out[(8 * rl + e) * PITCH + team] = c;
             if (p.values) {
-                decode8(c, s, x);
+                decode4(c, s, x);
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
+                for (int q = 0; q < 4; ++q)
                     v[q][e] = x[q];
             }
             if (BLOCK == 1 && team == 0 && e < n)
                 p.scales[(mat * p.R + r0 + e) * p.chunks + chunk] = s.s;
             if (BLOCK == 128 && e == 0 && threadIdx.x == 0)
-                p.scales[(mat * blocks + rb) * p.chunks + chunk] = s.s;
+                p.scales[(mat * groups + rb) * p.chunks + chunk] = s.s;
         }
         if (p.values) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int64_t k = k0 + 64 * (q >> 2) + (q & 3);
-                store8<BF16>(p.values, base + k * p.R + r0, k < p.K ? n : 0, v[q]);
-            }
+            for (int q = 0; q < 4; ++q)
+                store8<BF16>(p.values, base + (k0 + q) * p.R + r0, q < left ? n : 0, v[q]);
         }
         __syncthreads();
         // eight threads a row, sixteen codes each
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int r = q * 32 + (threadIdx.x >> 3), at = r * PITCH + 4 * (threadIdx.x & 7);
-            if (rb * 128 + r < p.R)
-                *reinterpret_cast<u32x4_t*>(p.codes + (mat * p.R + rb * 128 + r) * Kp + chunk * 128 +
+        for (int q = 0; q < ROWS * 8 / Cf::THREADS; ++q) {
+            const int r = q * (Cf::THREADS / 8) + (threadIdx.x >> 3), at = r * PITCH + 4 * (threadIdx.x & 7);
+            if (rb * ROWS + r < p.R)
+                *reinterpret_cast<u32x4_t*>(p.codes + (mat * p.R + rb * ROWS + r) * Kp + chunk * 128 +
                                             16 * (threadIdx.x & 7)) = u32x4_t{out[at], out[at + 1], out[at + 2], out[at + 3]};
         }
     }
@@ -392,9 +396,11 @@ static int launch_quantize(F8QuantParams p, int64_t count, int block, bool along
         return dim3((unsigned)std::min<int64_t>(works, 1 << 22));
     };
     if (!along && block == 1)
-        hipLaunchKernelGGL((fp8_quantize_across_kernel<BF16, 1>), grid(blocks), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((fp8_quantize_across_kernel<BF16, 1>), grid(count * ceil_div(p.R, 64) * p.chunks),
+                           dim3((unsigned)Across<BF16, 1>::THREADS), 0, s, p);
     else if (!along)
-        hipLaunchKernelGGL((fp8_quantize_across_kernel<BF16, 128>), grid(blocks), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((fp8_quantize_across_kernel<BF16, 128>), grid(blocks), dim3((unsigned)Across<BF16, 128>::THREADS), 0, s,
+                           p);
     else if (block == 128)
         hipLaunchKernelGGL((fp8_quantize_along_kernel<BF16, 128, 8>), grid(blocks), dim3(256), 0, s, p);
     else if (chunks < kManyChunks)

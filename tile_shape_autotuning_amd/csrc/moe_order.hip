@@ -432,39 +432,42 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(CombineParams p)
     }
 }
 
-// Rows of up to 1 KiB: sixteen lanes take a token, lane j of them has its j-th
-// row, and the four tokens of a wave go their own ways.
-constexpr int64_t kNarrow = 1024;
+// Shorter rows: TEAM lanes take a token, lane j of them has its j-th row, and a
+// wave's tokens go their own ways.  Sixteen lanes for rows of up to 1 KiB
+// (16384 x 8 rows of 128 bf16: 7 us, with a wave for each KiB 21; gradients 18, with
+// a workgroup a token 138), a wave for gradients of up to 2 KiB (520 bf16: 132 us, 167
+// with a workgroup).
+constexpr int64_t kTeamBytes = 1024, kWaveBytes = 2048;
 
-template <int KM>
+template <int KM, int TEAM>
 struct TeamRows {
     int r[KM];
     float w[KM];
     __device__ __forceinline__ TeamRows(const CombineParams& p, int64_t t, int lane)
     {
-        const int l = lane & 15;
+        const int l = lane & (TEAM - 1), first = lane & (64 - TEAM);
         const bool has = t < p.T && l < p.k;
         const int at = has ? p.position[t * p.k + l] : -1;
         const float wl = has && p.weights ? p.weights[t * p.k + l] : 1.0f;
 #pragma unroll
         for (int j = 0; j < KM; ++j) {                 // every lane runs here
-            const int v = __shfl(at, (lane & 48) | j);
+            const int v = __shfl(at, first | j);
             r[j] = v < p.rows ? v : -1;
-            w[j] = __shfl(wl, (lane & 48) | j);
+            w[j] = __shfl(wl, first | j);
         }
     }
 };
 
-template <bool BF16, int KM>
+template <bool BF16, int KM, int TEAM>
 __global__ void __launch_bounds__(256) moe_combine_narrow_kernel(CombineParams p)
 {
     using S = Slice<BF16>;
     const int lane = threadIdx.x & 63;
-    for (int64_t t0 = (int64_t)blockIdx.x * 16; t0 < p.T; t0 += (int64_t)gridDim.x * 16) {
-        const int64_t t = t0 + (threadIdx.x >> 4);
-        const TeamRows<KM> rows(p, t, lane);
-        for (int64_t h0 = 0; h0 < p.H; h0 += 16 * S::N) {
-            const int64_t h = h0 + (lane & 15) * S::N;
+    for (int64_t t0 = (int64_t)blockIdx.x * (256 / TEAM); t0 < p.T; t0 += (int64_t)gridDim.x * (256 / TEAM)) {
+        const int64_t t = t0 + (threadIdx.x / TEAM);
+        const TeamRows<KM, TEAM> rows(p, t, lane);
+        for (int64_t h0 = 0; h0 < p.H; h0 += TEAM * S::N) {
+            const int64_t h = h0 + (lane & (TEAM - 1)) * S::N;
             S x[KM], y;
 #pragma unroll
             for (int j = 0; j < KM; ++j)
@@ -485,17 +488,17 @@ __global__ void __launch_bounds__(256) moe_combine_narrow_kernel(CombineParams p
     }
 }
 
-template <bool BF16, int KM>
+template <bool BF16, int KM, int TEAM>
 __global__ void __launch_bounds__(256) moe_combine_grad_narrow_kernel(CombineParams p)
 {
     using S = Slice<BF16>;
     const int lane = threadIdx.x & 63;
-    for (int64_t t0 = (int64_t)blockIdx.x * 16; t0 < p.T; t0 += (int64_t)gridDim.x * 16) {
-        const int64_t t = t0 + (threadIdx.x >> 4);
-        const TeamRows<KM> rows(p, t, lane);
+    for (int64_t t0 = (int64_t)blockIdx.x * (256 / TEAM); t0 < p.T; t0 += (int64_t)gridDim.x * (256 / TEAM)) {
+        const int64_t t = t0 + (threadIdx.x / TEAM);
+        const TeamRows<KM, TEAM> rows(p, t, lane);
         float dot[KM] = {};
-        for (int64_t h0 = 0; h0 < p.H; h0 += 16 * S::N) {
-            const int64_t h = t < p.T ? h0 + (lane & 15) * S::N : p.H;
+        for (int64_t h0 = 0; h0 < p.H; h0 += TEAM * S::N) {
+            const int64_t h = t < p.T ? h0 + (lane & (TEAM - 1)) * S::N : p.H;
             S dy, x[KM];
             dy.load(row_at<BF16>(p.dy, t < p.T ? t : 0, p.H), h, p.H);
 #pragma unroll
@@ -517,9 +520,9 @@ __global__ void __launch_bounds__(256) moe_combine_grad_narrow_kernel(CombinePar
 #pragma unroll
         for (int j = 0; j < KM; ++j) {                 // every lane runs here
 #pragma unroll
-            for (int off = 1; off < 16; off <<= 1)
+            for (int off = 1; off < TEAM; off <<= 1)
                 dot[j] += __shfl_xor(dot[j], off);
-            if (t < p.T && (lane & 15) == j && j < p.k)
+            if (t < p.T && (lane & (TEAM - 1)) == j && j < p.k)
                 p.dweights[t * p.k + j] = dot[j];
         }
     }
@@ -528,8 +531,9 @@ __global__ void __launch_bounds__(256) moe_combine_grad_narrow_kernel(CombinePar
 template <bool BF16, int KM>
 static void launch_combine(const CombineParams& p, hipStream_t s)
 {
-    if (p.H * (BF16 ? 2 : 4) <= kNarrow)
-        hipLaunchKernelGGL((moe_combine_narrow_kernel<BF16, KM>), dim3(grid_of(ceil_div(p.T, 16))), dim3(256), 0, s, p);
+    if (p.H * (BF16 ? 2 : 4) <= kTeamBytes)
+        hipLaunchKernelGGL((moe_combine_narrow_kernel<BF16, KM, 16>), dim3(grid_of(ceil_div(p.T, 16))), dim3(256), 0, s,
+                           p);
     else
         hipLaunchKernelGGL((moe_combine_kernel<BF16, KM>), dim3(grid_of(ceil_div(p.T * p.pieces, 4))), dim3(256), 0, s,
                            p);
@@ -538,9 +542,13 @@ static void launch_combine(const CombineParams& p, hipStream_t s)
 template <bool BF16, int KM>
 static void launch_combine_grad(const CombineParams& p, hipStream_t s)
 {
-    if (p.H * (BF16 ? 2 : 4) <= kNarrow)
-        hipLaunchKernelGGL((moe_combine_grad_narrow_kernel<BF16, KM>), dim3(grid_of(ceil_div(p.T, 16))), dim3(256), 0, s,
-                           p);
+    const int64_t bytes = p.H * (BF16 ? 2 : 4);
+    if (bytes <= kTeamBytes)
+        hipLaunchKernelGGL((moe_combine_grad_narrow_kernel<BF16, KM, 16>), dim3(grid_of(ceil_div(p.T, 16))), dim3(256),
+                           0, s, p);
+    else if (bytes <= kWaveBytes)
+        hipLaunchKernelGGL((moe_combine_grad_narrow_kernel<BF16, KM, 64>), dim3(grid_of(ceil_div(p.T, 4))), dim3(256),
+                           0, s, p);
     else
         hipLaunchKernelGGL((moe_combine_grad_kernel<BF16, KM>), dim3(grid_of(p.T)), dim3(256), 0, s, p);
 }
