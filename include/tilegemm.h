@@ -575,8 +575,9 @@ int tg_fp8_quantize(int64_t count, int64_t R, int64_t K, int block, const void *
  * eight products, where the rounding to bf16 is off by up to 4e-3.  Rows and
  * columns with NaN codes or scales give NaN in their own results only.
  * workspace: device memory of tg_gemm_fp8_workspace_bytes(M, N, K), 16-byte
- * aligned (NULL where that is 0), not shared by calls that may overlap.  C must
- * not overlap the inputs.  The same call gives the same bits.
+ * aligned (NULL where that is 0, as for M <= 64), not shared by calls that may
+ * overlap; the size is for the device description in force.  C must not overlap
+ * the inputs.  The same call gives the same bits.
  * Limits: M, N <= 2^24, K <= 2^22 (TG_E_UNSUPPORTED).
  */
 int tg_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);

@@ -547,6 +547,119 @@ def test_a_layer_on_two_streams_and_in_two_graphs():
             assert all(torch.equal(a, b) for a, b in zip(r, w)), f"replay {turn}"
 
 
+def test_products_in_parts_in_two_graphs():
+    """The reduction in parts has a workspace for each call: two graphs and eager calls between their replays."""
+    rng = np.random.default_rng(12)
+    ins = []
+    for M, N, K in ((100, 1000, 9000), (70, 300, 5000)):
+        assert tg._native.gemm_fp8_workspace_bytes(M, N, K) > 0
+        A, a = _integers(rng, M, K, 1)
+        B, b = _integers(rng, N, K, 128)
+        ins.append((A, B, a @ b.T))
+    graphs, streams = [], [torch.cuda.Stream() for _ in ins]
+    for A, B, _ in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            C = tg.gemm_fp8(A, B, act="relu", out_dtype=torch.float32)
+        graphs.append((g, C))
+    for turn in range(3):
+        for (g, C), s in zip(graphs, streams):
+            C.fill_(-1.0)
+        torch.cuda.synchronize()
+        for (g, C), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        for A, B, want in ins:
+            assert np.array_equal(_np(tg.gemm_fp8(A, B, out_dtype=torch.float32)), want)
+        torch.cuda.synchronize()
+        for (g, C), (_, _, want) in zip(graphs, ins):
+            assert np.array_equal(_np(C), np.maximum(want, 0)), f"replay {turn}"
+
+
+@pytest.mark.parametrize("n_cu", [1, 7, 2 ** 31 - 1])
+def test_products_under_any_description(n_cu):
+    rng = np.random.default_rng(13)
+    desc = tg.get_device_desc()
+    desc.n_cu = n_cu
+    tg.set_device_override(desc)
+    try:
+        for M, N, K in ((100, 1000, 2000), (300, 600, 700), (5, 100, 300)):
+            A, a = _integers(rng, M, K, 1)
+            B, b = _integers(rng, N, K, 1)
+            assert np.array_equal(_np(tg.gemm_fp8(A, B, out_dtype=torch.float32)), a @ b.T)
+    finally:
+        tg.set_device_override(None)
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+def _far_matrix(lead, R_, K, block):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    codes = torch.randint(0x30, 0x48, (*lead, R_, K), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.full((*lead, -(-R_ // block), K // 128), 0.5, device="cuda")
+    return tg.F8(codes.view(E4M3), scales, K, block)
+
+
+def _values64(codes):
+    return R.VALUES[codes.view(torch.uint8).cpu().numpy()]
+
+
+def test_rows_past_32_bits_of_a_product():
+    K, M = 8192, 530000                                # 4.3e9 codes
+    A, B = _far_matrix((), M, K, 1), _far_matrix((), 16, K, 1)
+    C = tg.gemm_fp8(A, B, out_dtype=torch.float32)
+    a, b = _values64(A.codes[-70:]) * 0.5, _values64(B.codes) * 0.5
+    assert (np.abs(_np(C[-70:]) - a @ b.T) <= _bound(a, b, K)).all()
+
+
+def test_experts_past_32_bits():
+    E, N, K = 530, 1024, 8192                          # 4.4e9 codes
+    B = _far_matrix((E,), N, K, 128)
+    for n in (6, 600):
+        A = _far_matrix((), n, K, 1)
+        offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        offsets[E] = n                                 # all rows are the last expert's
+        C = tg.moe_gemm_fp8(A, B, offsets, out_dtype=torch.float32)
+        a, b = _values64(A.codes) * 0.5, _values64(B.codes[-1]) * 0.5
+        assert (np.abs(_np(C) - a @ b.T) <= _bound(a, b, K)).all()
+
+
+def test_rows_past_32_bits_of_copies_and_sums():
+    n, H = 600000, 4096                                # 4.9e9 bytes
+    rows = torch.empty((n, H), dtype=torch.bfloat16, device="cuda")
+    position = torch.tensor([[n - 1, 3], [n - 2, -1]], dtype=torch.int32, device="cuda")
+    order = tg.MoeOrder(position, position.view(-1), position.view(-1)[:1])
+    x = torch.randn((2, H), device="cuda").to(torch.bfloat16)
+    r = tg.moe_gather(x, order, out=rows)
+    assert torch.equal(r[n - 1], x[0]) and torch.equal(r[3], x[0]) and torch.equal(r[n - 2], x[1])
+    w = torch.tensor([[0.5, 0.25], [2.0, 9.0]], device="cuda")
+    y = tg.moe_combine(rows, order, w)
+    assert torch.equal(y, (x.float() * torch.tensor([[0.75], [2.0]], device="cuda")).to(torch.bfloat16))
+    dx, dw = tg.moe_combine_grad(x, rows, order, w, out=rows.clone())
+    assert torch.equal(dx[n - 1], x[0] / 2) and torch.equal(dx[n - 2], x[1] * 2)
+    own = (x.double() ** 2).sum(1)
+    assert float((dw.double() - torch.stack([own[[0, 0]], own[[1, 1]] * torch.tensor([1.0, 0.0], device="cuda")])).abs().max()) \
+        <= (H + 2) * 2.0 ** -24 * float(own.max())
+
+
+@pytest.mark.parametrize("along", [True, False])
+def test_quantize_past_32_bits(along):
+    R_, K = (530000, 8192) if along else (8192, 530000)
+    x = torch.zeros((R_, K) if along else (K, R_), dtype=torch.bfloat16, device="cuda")
+    x[-128:] = torch.randn((128, x.shape[1]), device="cuda").to(torch.bfloat16)
+    t = x if along else x.transpose(0, 1)
+    q = tg.fp8_quantize(t)
+    if along:
+        codes, scales = R.quantise(_np(x[-2:]), 1)
+        assert np.array_equal(_codes(q.codes[-2:]), codes) and np.array_equal(q.scales[-2:].cpu().numpy(), scales)
+    else:
+        # the last 80 of 530000 columns, in their own chunk, and the one before
+        codes, scales = R.quantise(_np(t[-3:, -80:]), 1)
+        assert K % 128 == 80 and np.array_equal(_codes(q.codes[-3:, -128:]), codes)
+        assert np.array_equal(q.scales[-3:, -1:].cpu().numpy(), scales)
+    assert not bool(q.codes[:1000].view(torch.uint8)[:, :128].any())
+
+
 def test_every_entry_point_takes_nothing():
     q = tg.fp8_quantize(torch.empty((0, 64), device="cuda"))
     assert q.codes.shape == (0, 128) and q.scales.shape == (0, 1)

@@ -128,7 +128,7 @@ def gemm_fp8(A, B, bias=None, act="none", out=None, out_dtype=None):
     if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_contiguous()
                              or bias.device != dev):
         raise ValueError("bias must be a contiguous float32 [N] tensor on A's device")
-    need = _native.gemm_fp8_workspace_bytes(M, N, K)
+    need = _native.gemm_fp8_workspace_bytes(M, N, K) if M > 64 else 0
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call(_native.gemm_fp8_ptr, dev, M, N, K, a, b, bias.data_ptr() if bias is not None else None, out.data_ptr(),
           BF16 if out.dtype == torch.bfloat16 else BF16_F32OUT,
