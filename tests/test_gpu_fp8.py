@@ -274,6 +274,34 @@ def test_gemm_writes_its_output_only():
             assert np.array_equal(_np(out), _held(a @ b.T, "bf16" if dt == torch.bfloat16 else "f32"))
 
 
+@pytest.mark.parametrize("M,N", [(3, 64), (300, 72), (1030, 2056), (2050, 4104)])
+def test_gemm_into_rows_off_alignment(M, N):
+    """Outputs that begin 2, 8 and 16 bytes past an aligned address: element, four- and eight-element stores."""
+    rng = np.random.default_rng(M)
+    A, a = _integers(rng, M, 136, 1)
+    B, b = _integers(rng, N, 136, 128)
+    want = R.round_bf16(a @ b.T)
+    for off in (1, 4, 8):
+        buf = torch.full((M * N + 32,), 9.0, device="cuda", dtype=torch.bfloat16)
+        out = buf[off:off + M * N].view(M, N)
+        tg.gemm_fp8(A, B, out=out)
+        assert np.array_equal(_np(out), want)
+        assert bool((buf[:off] == 9).all()) and bool((buf[off + M * N:] == 9).all())
+
+
+def test_experts_that_hardly_any_or_all_rows_are_for():
+    """Averages of few rows an expert, but one has them all; and the other way round."""
+    rng = np.random.default_rng(6)
+    for E, n in ((64, 1500), (300, 40)):
+        A, a = _integers(rng, n, 200, 1)
+        B, b = _integers(rng, 80, 200, 128, (E,))
+        offsets = np.zeros(E + 1, np.int32)
+        offsets[E // 2 + 1:] = n - 1
+        offsets[E] = n                                 # all but one in the middle, one at the end
+        C = _np(tg.moe_gemm_fp8(A, B, _cuda(offsets), out_dtype=torch.float32))
+        assert np.array_equal(C[:n - 1], a[:n - 1] @ b[E // 2].T) and np.array_equal(C[n - 1:], a[n - 1:] @ b[E - 1].T)
+
+
 def test_a_layers_gradients():
     """The three products of a training step against the formula on the values that the codes stand for."""
     rng = np.random.default_rng(10)

@@ -48,7 +48,8 @@ HEADERS = [os.path.join(CSRC, f) for f in ("select.hpp", "registry.hpp", "runtim
 
 # headers of the 4-bit, 8-bit and expert kernels only
 W4_HEADERS = [os.path.join(CSRC, f) for f in ("w4.hpp", "w4_host.hpp", "panel_stream.hpp", "moe.hpp", "fp8.hpp",
-                                              "fp8_host.hpp", "gemm_fp8_tiles.hpp", "gemm_fp8_stream.hpp")]
+                                              "fp8_host.hpp", "row_piece.hpp", "gemm_fp8_tiles.hpp",
+                                              "gemm_fp8_stream.hpp")]
 W4_SOURCES = ("w4_quantize.hip", "gemm_w4.hip", "moe.hip", "moe_up.hip", "moe_down.hip", "fp8_quantize.hip",
               "gemm_fp8.hip", "moe_order.hip")
 

@@ -19,6 +19,7 @@
 
 #include "fp8.hpp"
 #include "fp8_host.hpp"
+#include "row_piece.hpp"
 
 namespace tg {
 
@@ -34,44 +35,9 @@ struct F8QuantParams {
 };
 
 constexpr unsigned kInfBits = 0x7F800000u, kNanBits = 0x7FC00000u;
-typedef u32x4_t u32x4_any __attribute__((aligned(1)));
 typedef unsigned u32x2_t8 __attribute__((ext_vector_type(2)));
 
-// Eight neighbouring elements; those from `n` on are zero and are not written.
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&v)[8])
-{
-    if (n >= 8) {
-        if constexpr (BF16) {
-            const u32x4_t w = *reinterpret_cast<const u32x4_any*>(static_cast<const unsigned short*>(base) + at);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-        } else {
-            const u32x4_any* from = reinterpret_cast<const u32x4_any*>(static_cast<const float*>(base) + at);
-            const u32x4_t a = from[0], b = from[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = __uint_as_float(a[i]);
-                v[4 + i] = __uint_as_float(b[i]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = 0.0f;
-            if (i < n) {
-                if constexpr (BF16)
-                    v[i] = __uint_as_float((unsigned)static_cast<const unsigned short*>(base)[at + i] << 16);
-                else
-                    v[i] = static_cast<const float*>(base)[at + i];
-            }
-        }
-    }
-}
-
+// Eight neighbouring elements; those from `n` on are not written.
 template <bool BF16>
 __device__ __forceinline__ void store8(void* base, int64_t at, int n, const float (&v)[8])
 {
@@ -100,8 +66,9 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int n, const floa
 }
 
 // The largest |x| as bits: infinities and NaN are above every number.
-__device__ __forceinline__ unsigned top_of(const float (&v)[8], unsigned top)
+__device__ __forceinline__ unsigned top_of(const float (&v)[8])
 {
+    unsigned top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
@@ -201,7 +168,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_along_kernel(F8QuantParams p
     const int l16 = threadIdx.x & 15, team = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int64_t Kp = (int64_t)p.chunks * 128;
     for (int64_t work = blockIdx.x; work < p.works; work += gridDim.x) {
-        int64_t row[U], block = 0;
+        int64_t row[U], from[U], block = 0;            // rows past the last read the last
         int chunk[U];
         if constexpr (BLOCK == 1) {
 #pragma unroll
@@ -209,6 +176,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_along_kernel(F8QuantParams p
                 const unsigned g = (unsigned)(work * U + u) * 16 + team;
                 row[u] = g / (unsigned)p.chunks;
                 chunk[u] = (int)(g - (unsigned)row[u] * (unsigned)p.chunks);
+                from[u] = min(row[u], p.rows - 1);
             }
         } else {
             const int64_t blocks = (p.R + 127) / 128, rb = work / p.chunks, mat = rb / blocks;
@@ -217,19 +185,31 @@ __global__ void __launch_bounds__(256) fp8_quantize_along_kernel(F8QuantParams p
             for (int u = 0; u < U; ++u) {
                 const int64_t r = (rb - mat * blocks) * 128 + u * 16 + team;
                 row[u] = r < p.R ? mat * p.R + r : p.rows;
+                from[u] = mat * p.R + min(r, p.R - 1);
                 chunk[u] = (int)(work - rb * p.chunks);
             }
+        }
+        Piece<BF16, 8> x[U];
+        if (p.K >= 8) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u].load(static_cast<const char*>(p.x) + from[u] * p.K * (BF16 ? 2 : 4), chunk[u] * 128 + 8 * l16, p.K);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u].load_short(static_cast<const char*>(p.x) + from[u] * p.K * (BF16 ? 2 : 4), 8 * l16, p.K);
         }
         float v[U][8];
         unsigned top[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = chunk[u] * 128 + 8 * l16;
-            load8<BF16>(p.x, row[u] * p.K + k, row[u] < p.rows ? (int)min((int64_t)8, p.K - k) : 0, v[u]);
-        }
+            x[u].arrived();
+            x[u].end(chunk[u] * 128 + 8 * l16, p.K);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            top[u] = top_of(v[u], 0u);
+            for (int i = 0; i < 8; ++i)
+                v[u][i] = x[u][i];
+            top[u] = top_of(v[u]);
+        }
         if constexpr (BLOCK == 128) {
 #pragma unroll
             for (int u = 1; u < U; ++u)
@@ -300,10 +280,29 @@ __global__ void __launch_bounds__((Across<BF16, BLOCK>::THREADS), 4) fp8_quantiz
         const int64_t r0 = rb * ROWS + 8 * rl, k0 = chunk * 128 + 4 * team, base = mat * p.R * p.K;
         const int n = (int)max((int64_t)0, min((int64_t)8, p.R - r0));
         const int left = (int)max((int64_t)0, min((int64_t)4, p.K - k0));
+        // k past K read the last k: it is of this chunk
+        Piece<BF16, 8> in4[4];
+        auto from = [&](int q) {
+            return static_cast<const char*>(p.x) + (base + min(k0 + q, p.K - 1) * p.R) * (BF16 ? 2 : 4);
+        };
+        if (p.R >= 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                in4[q].load(from(q), r0, p.R);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                in4[q].load_short(from(q), r0, p.R);
+        }
         float v[4][8];                                 // [k][row]
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            load8<BF16>(p.x, base + (k0 + q) * p.R + r0, q < left ? n : 0, v[q]);
+        for (int q = 0; q < 4; ++q) {
+            in4[q].arrived();
+            in4[q].end(r0, p.R);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[q][e] = in4[q][e];
+        }
         unsigned top[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

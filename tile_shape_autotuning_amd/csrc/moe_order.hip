@@ -8,6 +8,7 @@
 #include <string>
 
 #include "kernels/common.hpp"
+#include "row_piece.hpp"
 #include "w4_host.hpp"
 
 namespace tg {
@@ -171,12 +172,14 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(SortParams p)
         }
         const int rank = __popcll(same & ((1ull << lane) - 1));
         const int r = has ? next[wave * p.E + e] + rank : -1;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");      // all lanes have read
         if (has && (same >> lane) == 1)                // the last of them
             next[wave * p.E + e] = r + 1;
         if (i < to)
             p.position[i] = r;
         if (has)
             p.source[r] = i;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -200,9 +203,6 @@ struct GatherParams {
     int64_t bytes[2];
 };
 
-// Sixteen bytes of any alignment: the memory takes them as they are.
-typedef u32x4_t u32x4_any __attribute__((aligned(1)));
-
 constexpr int kPiece = 4;                              // 16-byte loads of a lane
 
 // A wave reads a piece of a token's row once and writes it to each of the
@@ -212,15 +212,19 @@ __device__ __forceinline__ void gather_piece(const char* x, char* out, int64_t b
 {
     const int64_t items = bytes / 16, first = piece * 64 * kPiece + lane;
     const char* from = x + t * bytes;
-    u32x4_t v[kPiece];
+    u32x4_t v[kPiece] = {};
+    // lanes past the row read its last 16 bytes: a branch for them would wait for each load
 #pragma unroll
     for (int q = 0; q < kPiece; ++q)
-        if (first + 64 * q < items)
-            v[q] = reinterpret_cast<const u32x4_any*>(from)[first + 64 * q];
+        if (piece * 64 * kPiece + 64 * q < items)
+            v[q] = reinterpret_cast<const u32x4_any*>(from)[min(first + 64 * q, items - 1)];
     // what is left of the row after its whole 16 bytes
     const int rest = (int)(bytes & 15);
     const bool ends = rest && (piece + 1) * 64 * kPiece >= items && lane < rest;
     const char tail = ends ? from[items * 16 + lane] : (char)0;
+#pragma unroll
+    for (int q = 0; q < kPiece; ++q)
+        __asm__ __volatile__("" : "+v"(v[q]));
     for (int j = 0; j < k; ++j) {
         const int r = __builtin_amdgcn_readlane(at, j);
         if (r < 0)
@@ -270,40 +274,11 @@ struct CombineParams {
 };
 
 // A lane's 16 bytes of a row as fp32: 8 bf16 or 4 fp32, from element h on; those
-// past H are zero and are not written.
+// past H are not written.
 template <bool BF16>
 struct Slice {
     static constexpr int N = BF16 ? 8 : 4;
     float v[N];
-    __device__ __forceinline__ void load(const void* row, int64_t h, int64_t H)
-    {
-        if (h + N <= H) {
-            if constexpr (BF16) {
-                const u32x4_t w = *reinterpret_cast<const u32x4_any*>(static_cast<const unsigned short*>(row) + h);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                }
-            } else {
-                const u32x4_t w = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(row) + h);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = __uint_as_float(w[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                v[i] = 0.0f;
-                if (h + i < H) {
-                    if constexpr (BF16)
-                        v[i] = __uint_as_float((unsigned)static_cast<const unsigned short*>(row)[h + i] << 16);
-                    else
-                        v[i] = static_cast<const float*>(row)[h + i];
-                }
-            }
-        }
-    }
     __device__ __forceinline__ void store(void* row, int64_t h, int64_t H) const
     {
         if (h + N <= H) {
@@ -355,6 +330,45 @@ __device__ __forceinline__ char* row_at(const void* base, int64_t r, int64_t H)
     return const_cast<char*>(static_cast<const char*>(base)) + r * H * (BF16 ? 2 : 4);
 }
 
+// The parts of a token's rows from element h on, zeros for those that aren't there,
+// and of its gradient: all of them are on their way before the first is waited for.
+template <bool BF16, int KM>
+struct Parts {
+    Piece<BF16, Slice<BF16>::N> x[KM], dy;
+    __device__ __forceinline__ Parts(const CombineParams& p, const int (&r)[KM], int64_t h, const char* grad = nullptr)
+    {
+        dy.clear();
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+            x[j].clear();
+        if (p.H >= Slice<BF16>::N) {
+            if (grad)
+                dy.load(grad, h, p.H);
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (r[j] >= 0)
+                    x[j].load(row_at<BF16>(p.x, r[j], p.H), h, p.H);
+        } else {
+            if (grad)
+                dy.load_short(grad, h, p.H);
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (r[j] >= 0)
+                    x[j].load_short(row_at<BF16>(p.x, r[j], p.H), h, p.H);
+        }
+    }
+    __device__ __forceinline__ void arrived(int64_t h, int64_t H)
+    {
+        dy.arrived();
+        dy.end(h, H);
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            x[j].arrived();
+            x[j].end(h, H);
+        }
+    }
+};
+
 // A wave takes 1 KiB of a token's row: up to KM rows' parts are on their way at once.
 template <bool BF16, int KM>
 __global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
@@ -365,11 +379,8 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
     for (unsigned u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < units; u += gridDim.x * 4) {
         const int64_t t = u / (unsigned)p.pieces, h = (u - t * p.pieces) * 64 * S::N + lane * S::N;
         const Rows<KM> rows(p, t, lane);
-        S x[KM];
-#pragma unroll
-        for (int j = 0; j < KM; ++j)
-            if (rows.r[j] >= 0)
-                x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+        Parts<BF16, KM> in(p, rows.r, h);
+        in.arrived(h, p.H);
         S y;
 #pragma unroll
         for (int i = 0; i < S::N; ++i)
@@ -379,7 +390,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
             if (rows.r[j] >= 0)
 #pragma unroll
                 for (int i = 0; i < S::N; ++i)
-                    y.v[i] = fmaf(rows.w[j], x[j].v[i], y.v[i]);
+                    y.v[i] = fmaf(rows.w[j], in.x[j][i], y.v[i]);
         y.store(row_at<BF16>(p.y, t, p.H), h, p.H);
     }
 }
@@ -398,20 +409,16 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(CombineParams p)
         // the whole workgroup runs every step; threads past H load zeros and store nothing
         for (int64_t h0 = 0; h0 < p.H; h0 += 256 * S::N) {
             const int64_t h = h0 + threadIdx.x * S::N;
-            S dy, x[KM];
-            dy.load(row_at<BF16>(p.dy, t, p.H), h, p.H);
-#pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (rows.r[j] >= 0)
-                    x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+            Parts<BF16, KM> in(p, rows.r, h, row_at<BF16>(p.dy, t, p.H));
+            in.arrived(h, p.H);
 #pragma unroll
             for (int j = 0; j < KM; ++j)
                 if (rows.r[j] >= 0) {
                     S d;
 #pragma unroll
                     for (int i = 0; i < S::N; ++i) {
-                        dot[j] = fmaf(dy.v[i], x[j].v[i], dot[j]);
-                        d.v[i] = rows.w[j] * dy.v[i];
+                        dot[j] = fmaf(in.dy[i], in.x[j][i], dot[j]);
+                        d.v[i] = rows.w[j] * in.dy[i];
                     }
                     d.store(row_at<BF16>(p.dx, rows.r[j], p.H), h, p.H);
                 }
@@ -468,11 +475,9 @@ __global__ void __launch_bounds__(256) moe_combine_narrow_kernel(CombineParams p
         const TeamRows<KM, TEAM> rows(p, t, lane);
         for (int64_t h0 = 0; h0 < p.H; h0 += TEAM * S::N) {
             const int64_t h = h0 + (lane & (TEAM - 1)) * S::N;
-            S x[KM], y;
-#pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (rows.r[j] >= 0)
-                    x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+            Parts<BF16, KM> in(p, rows.r, h);
+            in.arrived(h, p.H);
+            S y;
 #pragma unroll
             for (int i = 0; i < S::N; ++i)
                 y.v[i] = 0.0f;
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(256) moe_combine_narrow_kernel(CombineParams p
                 if (rows.r[j] >= 0)
 #pragma unroll
                     for (int i = 0; i < S::N; ++i)
-                        y.v[i] = fmaf(rows.w[j], x[j].v[i], y.v[i]);
+                        y.v[i] = fmaf(rows.w[j], in.x[j][i], y.v[i]);
             if (t < p.T)
                 y.store(row_at<BF16>(p.y, t, p.H), h, p.H);
         }
@@ -499,20 +504,16 @@ __global__ void __launch_bounds__(256) moe_combine_grad_narrow_kernel(CombinePar
         float dot[KM] = {};
         for (int64_t h0 = 0; h0 < p.H; h0 += TEAM * S::N) {
             const int64_t h = t < p.T ? h0 + (lane & (TEAM - 1)) * S::N : p.H;
-            S dy, x[KM];
-            dy.load(row_at<BF16>(p.dy, t < p.T ? t : 0, p.H), h, p.H);
-#pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (rows.r[j] >= 0)
-                    x[j].load(row_at<BF16>(p.x, rows.r[j], p.H), h, p.H);
+            Parts<BF16, KM> in(p, rows.r, h, row_at<BF16>(p.dy, t < p.T ? t : 0, p.H));
+            in.arrived(h, p.H);
 #pragma unroll
             for (int j = 0; j < KM; ++j)
                 if (rows.r[j] >= 0) {
                     S d;
 #pragma unroll
                     for (int i = 0; i < S::N; ++i) {
-                        dot[j] = fmaf(dy.v[i], x[j].v[i], dot[j]);
-                        d.v[i] = rows.w[j] * dy.v[i];
+                        dot[j] = fmaf(in.dy[i], in.x[j][i], dot[j]);
+                        d.v[i] = rows.w[j] * in.dy[i];
                     }
                     d.store(row_at<BF16>(p.dx, rows.r[j], p.H), h, p.H);
                 }
