@@ -97,6 +97,12 @@ struct Scale {
         t = s * by;
         inv = t > 0.0f ? 1.0f / t : 0.0f;
     }
+    // one that another thread has worked out
+    __device__ __forceinline__ Scale(float s_, float inv_) : s(s_), inv(inv_)
+    {
+        by = s < 0x1p-100f ? 0x1p100f : 1.0f;
+        t = s * by;
+    }
 };
 
 // Codes of four elements whose estimates' ends differ somewhere (lo, hi).
@@ -253,10 +259,11 @@ __global__ void __launch_bounds__(256) fp8_quantize_along_kernel(F8QuantParams p
 }
 
 // x [K][R]: a workgroup takes 128 k of ROWS rows, a thread eight neighbouring rows
-// of four neighbouring k.  64 rows where they need no common scale: 32 elements a
-// thread and four workgroups a compute unit (4096 x 8192 bf16 with values 49 us;
-// 128 rows of eight k a thread leave two, which load, compute and store one after
-// the other, 75 us; workgroups numbered along k instead of the rows 70).
+// of four neighbouring k.  64 rows where they need no common scale: more, smaller
+// workgroups a compute unit load, compute and store beside each other; one thread a
+// row works out its scale for the others (4096 x 8192 bf16 with values 36 us, 4.6
+// TB/s; every thread for itself 41, and 128 rows that way 55).  Workgroups
+// numbered along k instead of the rows took 1.4 times as long.
 template <bool BF16, int BLOCK>
 struct Across {
     static constexpr int ROWS = BLOCK == 1 ? 64 : 128;
@@ -271,6 +278,7 @@ __global__ void __launch_bounds__((Across<BF16, BLOCK>::THREADS), 4) fp8_quantiz
     constexpr int ROWS = Cf::ROWS, LANES = Cf::LANES, PITCH = 33;   // dwords of a row of codes: other banks for the next
     __shared__ unsigned out[ROWS * PITCH];
     __shared__ unsigned tops[BLOCK == 1 ? Cf::WAVES * ROWS : Cf::WAVES];
+    __shared__ float scales[BLOCK == 1 ? 2 * ROWS : 1];             // and the reciprocals
     const int rl = threadIdx.x % LANES, team = threadIdx.x / LANES, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t Kp = (int64_t)p.chunks * 128, groups = (p.R + ROWS - 1) / ROWS;
     for (int64_t work = blockIdx.x; work < p.works; work += gridDim.x) {
@@ -321,11 +329,18 @@ __global__ void __launch_bounds__((Across<BF16, BLOCK>::THREADS), 4) fp8_quantiz
                 for (int e = 0; e < 8; ++e)
                     tops[wave * ROWS + 8 * rl + e] = top[e];
             __syncthreads();
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
+            if (threadIdx.x < ROWS) {
+                unsigned t = 0;
 #pragma unroll
                 for (int w = 0; w < Cf::WAVES; ++w)
-                    top[e] = max(top[e], tops[w * ROWS + 8 * rl + e]);
+                    t = max(t, tops[w * ROWS + threadIdx.x]);
+                const Scale s(t);
+                scales[threadIdx.x] = s.s;
+                scales[ROWS + threadIdx.x] = s.inv;
+                if (rb * ROWS + (int)threadIdx.x < p.R)
+                    p.scales[(mat * p.R + rb * ROWS + threadIdx.x) * p.chunks + chunk] = s.s;
+            }
+            __syncthreads();
         } else {
             unsigned t = top[0];
 #pragma unroll
@@ -338,13 +353,11 @@ __global__ void __launch_bounds__((Across<BF16, BLOCK>::THREADS), 4) fp8_quantiz
 #pragma unroll
             for (int w = 0; w < Cf::WAVES; ++w)
                 t = max(t, tops[w]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                top[e] = t;
+            top[0] = t;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const Scale s(top[e]);
+            const Scale s = BLOCK == 1 ? Scale(scales[8 * rl + e], scales[ROWS + 8 * rl + e]) : Scale(top[0]);
             float x[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -358,8 +371,6 @@ __global__ void __launch_bounds__((Across<BF16, BLOCK>::THREADS), 4) fp8_quantiz
                 for (int q = 0; q < 4; ++q)
                     v[q][e] = x[q];
             }
-            if (BLOCK == 1 && team == 0 && e < n)
-                p.scales[(mat * p.R + r0 + e) * p.chunks + chunk] = s.s;
             if (BLOCK == 128 && e == 0 && threadIdx.x == 0)
                 p.scales[(mat * groups + rb) * p.chunks + chunk] = s.s;
         }

@@ -441,9 +441,10 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(CombineParams p)
 
 // Shorter rows: TEAM lanes take a token, lane j of them has its j-th row, and a
 // wave's tokens go their own ways.  Sixteen lanes for rows of up to 1 KiB
-// (16384 x 8 rows of 128 bf16: 7 us, with a wave for each KiB 21; gradients 18, with
-// a workgroup a token 138), a wave for gradients of up to 2 KiB (520 bf16: 132 us, 167
-// with a workgroup).
+// (16384 x 8 rows of 128 bf16: 6 us, with a wave for each KiB 12; gradients 15, with
+// a wave a token 37, a workgroup 74; 300 x 8 rows of 768 would take 13, with a
+// wave 9), a wave for gradients of up to 2 KiB (16384 x 2 rows of 1024 bf16: 28 us, 40
+// with a workgroup; 16384 x 8: 114 and 111).
 constexpr int64_t kTeamBytes = 1024, kWaveBytes = 2048;
 
 template <int KM, int TEAM>
