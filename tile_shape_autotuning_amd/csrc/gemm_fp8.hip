@@ -185,8 +185,8 @@ struct TilePlan {
 
 // The tile, and into how many parts the reduction is split, with the smallest
 // estimate: rounds of workgroups on the compute units times what they take, and
-// for parts a second launch that adds up their slabs.  Without parts 100 x 1000 x 16384 takes 45 us, 32
-// workgroups of 128 chunks.
+// for parts a second launch that adds up their slabs.  Without parts 100 x 1000 x
+// 16384 takes 45 us, 32 workgroups of 128 chunks.
 static TilePlan plan_tiles(int64_t M, int64_t N, int chunks, int64_t experts, int form)
 {
     TilePlan best{kTile128, 1, chunks};

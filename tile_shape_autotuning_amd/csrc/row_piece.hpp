@@ -31,13 +31,15 @@ struct Piece {
             v[q] = u32x4_t{0, 0, 0, 0};
     }
     // Elements h .. h + N - 1 of `row`, which has H >= N; arrived() and end(h, H) have to follow.
+    // ONCE: it is not read again soon, and need not stay in the caches.
+    template <bool ONCE = false>
     __device__ __forceinline__ void load(const void* row, int64_t h, int64_t H)
     {
         const int64_t at = min(h, H - N) * (BF16 ? 2 : 4);
         const u32x4_any* from = reinterpret_cast<const u32x4_any*>(static_cast<const char*>(row) + at);
 #pragma unroll
         for (int q = 0; q < D / 4; ++q)
-            v[q] = from[q];
+            v[q] = ONCE ? __builtin_nontemporal_load(from + q) : from[q];
     }
     // The same of a row with H < N.
     __device__ __forceinline__ void load_short(const void* row, int64_t h, int64_t H)
