@@ -133,6 +133,35 @@ def test_quantize_the_transpose_is_the_transpose_of_blocks():
     assert torch.equal(a.codes[:, :270].view(torch.uint8), b.codes[:, :400].view(torch.uint8).t())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("along", [True, False])
+def test_quantize_every_short_length(dtype, along):
+    """Rows of 1 to 19 elements (of 1 to 19 matrices' columns) between elements that are not numbers."""
+    rng = np.random.default_rng(19)
+    for n in range(1, 20):
+        x = _held(rng.standard_normal((9, n)), dtype)
+        buf = torch.full((9 * n + 14,), float("nan"), device="cuda", dtype=_dtype(dtype))
+        t = buf[7:7 + 9 * n].view(9, n)
+        t.copy_(_put(x, dtype))
+        view, want = (t, x) if along else (t.transpose(0, 1), x.T)
+        for block in (1, 128):
+            q, values = tg.fp8_quantize(view, block, values=True)
+            codes, scales = R.quantise(np.ascontiguousarray(want), block)
+            assert np.array_equal(q.scales.cpu().numpy(), scales) and np.array_equal(_codes(q.codes), codes), n
+            v = _held(R.dense(codes, scales, want.shape[1], block).astype(np.float32), dtype)
+            assert np.array_equal(_np(values), v), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_many_rows(dtype):
+    """More chunks than a lane takes one at a time, the last ones ragged in rows and in K."""
+    rng = np.random.default_rng(8)
+    x = _held(rng.standard_normal((8003, 1030)) * 10.0 ** rng.uniform(-3, 3, (8003, 1)), dtype)
+    q = tg.fp8_quantize(_put(x, dtype))
+    codes, scales = R.quantise(x, 1)
+    assert np.array_equal(q.scales.cpu().numpy(), scales) and np.array_equal(_codes(q.codes), codes)
+
+
 def test_quantize_a_view_off_16_bytes():
     base = torch.randn(70 * 256 + 3, device="cuda").to(torch.bfloat16)
     for off in (1, 3):
@@ -453,6 +482,43 @@ def test_combine_gradient_agrees_with_differences():
         want = float((grad.double() * d.double()).sum())
         size = float((dy.abs().double() * (hi.abs() + lo.abs()).double()).sum()) + float(grad.abs().double().sum())
         assert abs(got - want) <= (2 * k + H + 4) * 2.0 ** -23 * (size + float(dy.abs().sum()) * k * 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_every_short_width(dtype):
+    """Rows of small integers of 1 to 40 elements, and about the widths where other kernels take over, off
+    alignment between elements that are not numbers: sums are exact."""
+    rng = np.random.default_rng(40)
+    T, k, E = 13, 3, 4
+    ids = _ids(rng, T, E, k, "away")
+    order = tg.moe_sort(_cuda(ids), E)
+    position = order.position.cpu().numpy()
+    has = position >= 0
+    n = int(has.sum())
+    w = rng.integers(1, 5, (T, k)).astype(np.float32)
+
+    def between(a):
+        buf = torch.full((a.size + 10,), float("nan"), device="cuda", dtype=_dtype(dtype))
+        t = buf[5:5 + a.size].view(a.shape)
+        t.copy_(_put(a, dtype))
+        return t
+
+    for H in (*range(1, 41), 255, 257, 511, 513, 1023, 1025, 1031, 2049, 2055):
+        x, dy = rng.integers(-4, 5, (T * k, H)).astype(np.float64), rng.integers(-4, 5, (T, H)).astype(np.float64)
+        x[n:] = np.nan                                 # rows behind the last
+        rows = np.where(has[..., None], np.nan_to_num(x)[position], 0.0)
+        tx, tdy = between(x), between(dy)
+        y = tg.moe_combine(tx, order, _cuda(w))
+        assert np.array_equal(_np(y), _held((w[..., None] * rows).sum(1), dtype)), H
+        dx, dw = tg.moe_combine_grad(tdy, tx, order, _cuda(w), out=torch.full_like(tx, 7.0))
+        want = np.full((T * k, H), 7.0)
+        want[position[has]] = (w[..., None] * dy[:, None])[has]
+        assert np.array_equal(_np(dx), _held(want, dtype)), H
+        assert np.array_equal(_np(dw), np.where(has, (dy[:, None] * rows).sum(2), 0.0)), H
+        out = torch.full((T * k, H), 7.0, device="cuda", dtype=_dtype(dtype))
+        tg.moe_gather(tdy, order, out=out)
+        want[position[has]] = np.repeat(dy[:, None], k, 1)[has]
+        assert np.array_equal(_np(out), want), H
 
 
 # ---------------------------------------------------------------- experts
