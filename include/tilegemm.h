@@ -37,7 +37,8 @@ typedef enum {
     TG_E_CACHE = -6         /* tuning-cache file missing, unreadable or malformed */
 } tg_status;
 
-/* input -> output element types; accumulation is always fp32 */
+/* input -> output element types; accumulation is always fp32 (TG_FAST_SUMS, which a call on 8-bit matrices may ask for,
+ * is the one exception) */
 typedef enum {
     TG_F32 = 0,          /* fp32 in, fp32 out */
     TG_BF16 = 1,         /* bf16 in, bf16 out (round to nearest even) */
@@ -538,6 +539,9 @@ typedef struct {
     int32_t block, reserved;
 } tg_f8;
 
+/* Added to the dtype of C in a call of tg_gemm_fp8 or tg_moe_gemm_fp8: see there. */
+#define TG_FAST_SUMS 0x100
+
 /*
  * Quantises `count` R x K matrices.  x: fp32 or bf16 (dtype = TG_F32 or
  * TG_BF16), each matrix [R][K] if rows_first, else [K][R] (the transpose is
@@ -567,13 +571,15 @@ int tg_fp8_quantize(int64_t count, int64_t R, int64_t K, int block, const void *
  * transposes of output gradients and of activations (both block 1) the weights'.
  * Products of codes are summed 128 k at a time, and those sums times the fp32
  * product of their two scales are added up in fp32: scales whose product is
- * below 2^-126 lose bits, above 2^128 they give infinities.  An fp32 C has all
- * its sums in fp32.  A bf16 C may have the sums of a chunk from the 8-bit form of
- * the matrix cores, which cuts each eight products to multiples of 2^-13 of
- * (the power of two of) the largest before it adds them in fp32: results are off
- * by 2e-5 of their size in the mean, at most by 7/8192 of the largest of each
- * eight products, where the rounding to bf16 is off by up to 4e-3.  Rows and
- * columns with NaN codes or scales give NaN in their own results only.
+ * below 2^-126 lose bits, above 2^128 they give infinities (NaN where the sum is
+ * 0).  Products of codes are exact and all sums are fp32, whatever M and the type of
+ * C.  With TG_FAST_SUMS added to dtype the sums of 128 k may come from the 8-bit form
+ * of the matrix cores (for M > 64), at up to twice the rate: it cuts each
+ * eight products, of k = 8 j .. 8 j + 7, to multiples of 2^-13 of (the power of two
+ * of) the largest before it adds them in fp32.  Results are then off by up to
+ * 7/8192 of the largest of each eight products; where products cancel that can be
+ * all of the result.  Rows and columns with NaN codes or scales give NaN in their
+ * own results only.
  * workspace: device memory of tg_gemm_fp8_workspace_bytes(M, N, K), 16-byte
  * aligned (NULL where that is 0, as for M <= 64), not shared by calls that may
  * overlap; the size is for the device description in force.  C must not overlap
@@ -616,7 +622,8 @@ int tg_moe_gather(int64_t T, int k, int64_t rows, const int32_t *position, int64
  * in offsets[e] .. offsets[e + 1] - 1.  A: `rows` x K, block 1; B: a stack of E
  * matrices N x K; C: rows x N, bf16 or fp32.  offsets: E + 1 int32 on the device,
  * rising; what they name outside [0, rows) is skipped.  Rows outside every
- * expert's are not read, and left as they were in C.
+ * expert's are not read, and left as they were in C.  TG_FAST_SUMS may be added to
+ * dtype, with effect for more than 32 rows an expert on average.
  * Limits: E <= 1024, rows, N <= 2^24, K <= 2^22 (TG_E_UNSUPPORTED).
  */
 int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8 *A, const tg_f8 *B,

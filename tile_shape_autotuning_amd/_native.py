@@ -13,6 +13,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libtilegemm.so")
 
 F32, BF16, BF16_F32OUT = 0, 1, 2
+FAST_SUMS = 0x100                                      # added to the dtype of a product of 8-bit matrices
 W_BF16, W_W4 = 0, 1
 GATE = {"silu": 0, "gelu": 1}
 ACT = {"none": 0, "relu": 1, "gelu": 2}

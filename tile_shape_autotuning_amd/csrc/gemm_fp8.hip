@@ -5,9 +5,9 @@
 //
 // A chunk of 128 k of 16 x 16 results is summed from zero; a lane's four sums are
 // multiplied by their scales as they are added up, in fp32.  B is the first
-// operand: a lane then has one row m and four neighbouring columns n.  fp32
-// results and few rows take the exact form of the products, bf16 results of many
-// rows the fast one (fp8.hpp).
+// operand: a lane then has one row m and four neighbouring columns n.  Products
+// take the exact form; those of many rows the fast one where the caller asks for
+// it (fp8.hpp).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -248,12 +248,12 @@ static int64_t stream_rows(int64_t M, int64_t experts)
     return experts ? ceil_div(M, std::min(experts, M)) : M;
 }
 
-static int launch_gemm(F8Params p, void* workspace, size_t workspace_bytes, hipStream_t s)
+static int launch_gemm(F8Params p, bool exact, void* workspace, size_t workspace_bytes, hipStream_t s)
 {
     p.group_m = 8;
     p.vec_out = p.N % 4 == 0 && (uintptr_t)p.C % (p.out_bf16 ? 8 : 16) == 0;
     p.line_out = p.N % 8 == 0 && (uintptr_t)p.C % 16 == 0;
-    const bool by_rows = p.b_rows == 1, exact = !p.out_bf16;
+    const bool by_rows = p.b_rows == 1;
     const int64_t experts = p.offsets ? std::min<int64_t>(p.E, p.M) : 0, rows = stream_rows(p.M, experts);
     if (rows <= (experts ? kStreamExpertRows : kStreamRows))
         return by_rows ? stream_by_rows<true>(p, rows, s) : stream_by_rows<false>(p, rows, s);
@@ -280,11 +280,14 @@ static int launch_gemm(F8Params p, void* workspace, size_t workspace_bytes, hipS
     return e == hipSuccess ? TG_OK : set_hip_error(e, "gemm_fp8 sums launch");
 }
 
+// The type of C in a dtype that may have TG_FAST_SUMS.
+static int c_type(int dtype) { return dtype & ~TG_FAST_SUMS; }
+
 static int check_product(int64_t M, int64_t N, int64_t K, int dtype)
 {
     if (M < 0 || N < 0 || K < 1)
         return set_error(TG_E_INVAL, "rows and N must be >= 0, K >= 1");
-    if (dtype != TG_BF16 && dtype != TG_BF16_F32OUT)
+    if (c_type(dtype) != TG_BF16 && c_type(dtype) != TG_BF16_F32OUT)
         return set_error(TG_E_INVAL, "C is bf16 (TG_BF16) or fp32 (TG_BF16_F32OUT)");
     if (M > kMaxSide || N > kMaxSide || K > kMaxDepth)
         return set_error(TG_E_UNSUPPORTED, "rows and N are at most 2^24, K 2^22");
@@ -293,7 +296,7 @@ static int check_product(int64_t M, int64_t N, int64_t K, int dtype)
 
 static int check_output(const void* C, int dtype)
 {
-    if (!C || ((uintptr_t)C & (dtype == TG_BF16 ? 1u : 3u)))
+    if (!C || ((uintptr_t)C & (c_type(dtype) == TG_BF16 ? 1u : 3u)))
         return set_error(TG_E_INVAL, "C must be given, aligned to its elements");
     return TG_OK;
 }
@@ -310,7 +313,7 @@ static F8Params params_of(int64_t M, int64_t N, int64_t K, const tg_f8& A, const
     p.N = N;
     p.chunks = (int)ceil_div(K, 128);
     p.b_rows = B.block;
-    p.out_bf16 = dtype == TG_BF16;
+    p.out_bf16 = c_type(dtype) == TG_BF16;
     return p;
 }
 
@@ -351,7 +354,7 @@ int tg_gemm_fp8(int64_t M, int64_t N, int64_t K, const tg_f8* A, const tg_f8* B,
     F8Params p = params_of(M, N, K, *A, *B, C, dtype);
     p.bias = bias;
     p.act = act;
-    return launch_gemm(p, workspace, workspace_bytes, current_stream());
+    return launch_gemm(p, !(dtype & TG_FAST_SUMS), workspace, workspace_bytes, current_stream());
 }
 
 int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8* A, const tg_f8* B,
@@ -376,7 +379,7 @@ int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8* 
     F8Params p = params_of(rows, N, K, *A, *B, C, dtype);
     p.offsets = offsets;
     p.E = (int)E;
-    return launch_gemm(p, nullptr, 0, current_stream());
+    return launch_gemm(p, !(dtype & TG_FAST_SUMS), nullptr, 0, current_stream());
 }
 
 }  // extern "C"

@@ -5,8 +5,8 @@
 // the chunks of 128 k into W neighbouring ranges, and their sums meet in LDS at
 // the end.  Each wave has a ring of R chunks in LDS to itself, panels, rows and
 // scales, which it fills R chunks ahead without registers and without barriers.  The
-// products are the exact form for bf16 results too: the conversions are hidden
-// behind the stream (16 x 28672 x 8192 44.7 us, with the fast form 44.2).
+// products are the exact form in every call: the conversions are hidden behind
+// the stream (16 x 28672 x 8192 44.7 us, with the fast form 44.2).
 #pragma once
 
 #include "fp8.hpp"

@@ -287,7 +287,7 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, char* lds, int64_t m0
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    if constexpr (Cf::WN % 64 == 0 && !EXACT) {
+    if constexpr (Cf::WN % 64 == 0) {
         if (p.out_bf16 && p.line_out) {
             // whole lines of bf16 through the wave's own part of the ring: eight
             // columns, 16 bytes, of row r at unit u ^ (r & 7) of each 128 bytes

@@ -11,7 +11,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 from . import _native
-from ._native import ACT, BF16, BF16_F32OUT, F32, F8Matrix
+from ._native import ACT, BF16, BF16_F32OUT, F32, FAST_SUMS, F8Matrix
 from .experts import _call, _int32
 
 
@@ -68,6 +68,10 @@ def _output(out, out_dtype, shape, device):
     return out
 
 
+def _c_type(out, fast_sums):
+    return (BF16 if out.element_size() == 2 else BF16_F32OUT) | (FAST_SUMS if fast_sums else 0)
+
+
 def fp8_quantize(x, block=1, values=False):
     """Quantises matrices [.., R, K] to 8 bits, with a scale for each 128
     elements of a row (block=1: activations) or for each block of 128 x 128
@@ -106,14 +110,15 @@ def fp8_quantize(x, block=1, values=False):
     return (q, out) if values else q
 
 
-def gemm_fp8(A, B, bias=None, act="none", out=None, out_dtype=None):
+def gemm_fp8(A, B, bias=None, act="none", out=None, out_dtype=None, fast_sums=False):
     """C = act(A @ B^T + bias) of two 8-bit matrices.
 
     A: an F8 of M x K, block 1; B: an F8 of N x K (a layer's output rows x input
     columns), block 1 or 128; bias: [N] float32 or None; act: "none" | "relu" |
-    "gelu"; out_dtype: torch.bfloat16 (default) or torch.float32, which also has
-    the more exact sums (tilegemm.h).  Runs on the current stream and returns C
-    [M, N].
+    "gelu"; out_dtype: torch.bfloat16 (default) or torch.float32.  All sums are
+    fp32; fast_sums=True lets the matrix cores' 8-bit form add up the products of
+    more than 64 rows, in up to half the time, which loses small products beside
+    large ones (tilegemm.h).  Runs on the current stream and returns C [M, N].
 
     A layer and its gradients, x [T, K], W [N, K], dy [T, N]:
       y  = gemm_fp8(fp8_quantize(x), fp8_quantize(W, 128))
@@ -131,20 +136,20 @@ def gemm_fp8(A, B, bias=None, act="none", out=None, out_dtype=None):
     need = _native.gemm_fp8_workspace_bytes(M, N, K) if M > 64 else 0
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call(_native.gemm_fp8_ptr, dev, M, N, K, a, b, bias.data_ptr() if bias is not None else None, out.data_ptr(),
-          BF16 if out.dtype == torch.bfloat16 else BF16_F32OUT,
+          _c_type(out, fast_sums),
           ACT[act] if isinstance(act, str) else _int32(int(act), "act"), ws.data_ptr() if need else None, need)
     return out
 
 
-def moe_gemm_fp8(A, B, offsets, out=None, out_dtype=None):
+def moe_gemm_fp8(A, B, offsets, out=None, out_dtype=None, fast_sums=False):
     """gemm_fp8 for each expert on its own rows: C[r] = A[r] @ B[e]^T for the
     rows r in offsets[e] .. offsets[e + 1] - 1.
 
     A: an F8 of n x K, block 1, rows in the order of moe_gather; B: an F8 [E, N,
     K], block 1 or 128; offsets: [E + 1] int32 (MoeOrder.offsets); out_dtype:
-    torch.bfloat16 (default) or torch.float32.  Rows that no expert has are
-    left as they were in `out`, and hold anything in a new tensor.  Returns C
-    [n, N].
+    torch.bfloat16 (default) or torch.float32; fast_sums: as in gemm_fp8, for more
+    than 32 rows an expert on average.  Rows that no expert has are left as they
+    were in `out`, and hold anything in a new tensor.  Returns C [n, N].
     """
     import torch
     a, n = _f8(A, 0, None, None, "A", (1,))
@@ -156,5 +161,5 @@ def moe_gemm_fp8(A, B, offsets, out=None, out_dtype=None):
         raise ValueError("offsets must be a contiguous int32 [E + 1] tensor on A's device")
     out = _output(out, out_dtype, (n, N), dev)
     _call(_native.moe_gemm_fp8_ptr, dev, n, E, N, K, a, b, offsets.data_ptr(), out.data_ptr(),
-          BF16 if out.dtype == torch.bfloat16 else BF16_F32OUT)
+          _c_type(out, fast_sums))
     return out
