@@ -47,7 +47,7 @@ typedef enum {
 
 typedef enum {
     TG_ACT_NONE = 0,
-    TG_ACT_RELU = 1,     /* max(0, x) */
+    TG_ACT_RELU = 1,     /* max(0, x); of a NaN 0, but a NaN in products of 8-bit matrices */
     TG_ACT_GELU = 2      /* 0.5 x (1 + erf(x / sqrt 2)) */
 } tg_act;
 
@@ -579,7 +579,7 @@ int tg_fp8_quantize(int64_t count, int64_t R, int64_t K, int block, const void *
  * of) the largest before it adds them in fp32.  Results are then off by up to
  * 7/8192 of the largest of each eight products; where products cancel that can be
  * all of the result.  Rows and columns with NaN codes or scales give NaN in their
- * own results only.
+ * own results only, with every act.
  * workspace: device memory of tg_gemm_fp8_workspace_bytes(M, N, K), 16-byte
  * aligned (NULL where that is 0, as for M <= 64), not shared by calls that may
  * overlap; the size is for the device description in force.  C must not overlap

@@ -23,6 +23,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/tilegemm.h"
 #include "kernels/common.hpp"
 
 namespace tg {
@@ -71,6 +72,14 @@ __device__ __forceinline__ f32x4_t mfma_exact(const Expanded& a, const Expanded&
     for (int i = 1; i < 4; ++i)
         d = mfma_bf16(a.v[i], b.v[i], d);
     return d;
+}
+
+// The activation of these products; a NaN stays one (apply_act's ReLU gives 0).
+__device__ __forceinline__ float activate(float v, int act)
+{
+    if (act == TG_ACT_RELU)
+        return v <= 0.0f ? 0.0f : v;
+    return act == TG_ACT_GELU ? gelu_erf(v) : v;
 }
 
 }  // namespace tg

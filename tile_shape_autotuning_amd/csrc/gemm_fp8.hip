@@ -105,6 +105,47 @@ __device__ __forceinline__ bool expert_tile(const F8Params& p, int tiles_n, int6
 
 namespace tg {
 
+// C = act(sums of the S parts of the reduction, in order, + bias): four
+// neighbouring results a thread, all of its loads on their way at once.  Bound by
+// memory: 4 S bytes read a result, once.  (splitk_reduce does the same for other
+// products, whose ReLU makes a NaN 0.)
+template <int S>
+__global__ void __launch_bounds__(256) gemm_fp8_parts_kernel(F8Params p)
+{
+    const int64_t n = p.M * p.N, stride = (int64_t)gridDim.x * 1024;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += stride) {
+        // slabs are whole fours: what is past the last result is read and not used
+        f32x4_t part[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            part[s] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p.slabs + s * p.slab + i));
+        f32x4_t v = part[0];
+#pragma unroll
+        for (int s = 1; s < S; ++s)
+            v += part[s];
+        int64_t col = p.bias ? i % p.N : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = activate(v[e] + (p.bias ? p.bias[col] : 0.0f), p.act);
+            col = col + 1 == p.N ? 0 : col + 1;
+        }
+        // as one row of n results
+        store_four(p, i, n - i, v);
+    }
+}
+
+static int launch_parts(const F8Params& p, hipStream_t s)
+{
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(p.M * p.N, 1024), 65536)), block(256);
+    switch (p.split) {
+    case 2: hipLaunchKernelGGL(gemm_fp8_parts_kernel<2>, grid, block, 0, s, p); break;
+    case 4: hipLaunchKernelGGL(gemm_fp8_parts_kernel<4>, grid, block, 0, s, p); break;
+    case 8: hipLaunchKernelGGL(gemm_fp8_parts_kernel<8>, grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL(gemm_fp8_parts_kernel<16>, grid, block, 0, s, p); break;
+    }
+    return launched("gemm_fp8 sums launch");
+}
+
 template <int BM, int BN, int WGM, int WGN, int ST, bool BROWS, bool EXACT>
 static int launch_tiles(const F8Params& p, hipStream_t s)
 {
@@ -258,7 +299,7 @@ static int launch_gemm(F8Params p, bool exact, void* workspace, size_t workspace
     if (rows <= (experts ? kStreamExpertRows : kStreamRows))
         return by_rows ? stream_by_rows<true>(p, rows, s) : stream_by_rows<false>(p, rows, s);
     const TilePlan t = plan_tiles(p.M, p.N, p.chunks, experts, 2 * exact + by_rows);
-    const F8Params whole = p;
+    F8Params whole = p;
     p.split = t.split;
     p.each = t.each;
     if (t.split > 1) {
@@ -276,8 +317,11 @@ static int launch_gemm(F8Params p, bool exact, void* workspace, size_t workspace
                          : by_rows ? launch_tile<true, false>(p, t.tile, s) : launch_tile<false, false>(p, t.tile, s);
     if (st != TG_OK || t.split == 1)
         return st;
-    const hipError_t e = splitk_reduce(p.slabs, t.split, whole.M, whole.N, whole.bias, whole.C, whole.out_bf16, whole.act, s);
-    return e == hipSuccess ? TG_OK : set_hip_error(e, "gemm_fp8 sums launch");
+    whole.split = t.split;
+    whole.slabs = p.slabs;
+    whole.slab = p.slab;
+    whole.vec_out = (uintptr_t)whole.C % (whole.out_bf16 ? 8 : 16) == 0;
+    return launch_parts(whole, s);
 }
 
 // The type of C in a dtype that may have TG_FAST_SUMS.

@@ -14,33 +14,38 @@
 
 namespace tg {
 
-// Four neighbouring results of a row.
-__device__ __forceinline__ void store_results(const F8Params& p, int64_t row, int64_t col, const f32x4_t& v)
+// Four neighbouring results from element `at` of C, of which the first `left` are there.
+__device__ __forceinline__ void store_four(const F8Params& p, int64_t at, int64_t left, const f32x4_t& v)
 {
-    const int64_t at = row * p.N + col;
     if (p.out_bf16) {
         unsigned short* to = static_cast<unsigned short*>(p.C) + at;
-        if (p.vec_out && col < p.N) {
+        if (p.vec_out && left >= 4) {
             typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
             *reinterpret_cast<u16x4*>(to) = u16x4{f32_to_bf16_rne(v[0]), f32_to_bf16_rne(v[1]), f32_to_bf16_rne(v[2]),
                                                   f32_to_bf16_rne(v[3])};
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (col + e < p.N)
+                if (e < left)
                     to[e] = f32_to_bf16_rne(v[e]);
         }
     } else {
         float* to = static_cast<float*>(p.C) + at;
-        if (p.vec_out && col < p.N) {
+        if (p.vec_out && left >= 4) {
             *reinterpret_cast<f32x4_t*>(to) = f32x4_t{v[0], v[1], v[2], v[3]};
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (col + e < p.N)
+                if (e < left)
                     to[e] = v[e];
         }
     }
+}
+
+// The same of a row.
+__device__ __forceinline__ void store_results(const F8Params& p, int64_t row, int64_t col, const f32x4_t& v)
+{
+    store_four(p, row * p.N + col, p.N - col, v);
 }
 
 // One wave-wide load of 4 bytes a lane straight into LDS (lane l writes lds_addr
@@ -182,7 +187,7 @@ __device__ __forceinline__ void f8_stream(const F8Params& p, char* lds, int64_t 
         if (row < m1 && col < p.N) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                sum[e] = apply_act(sum[e] + (p.bias && col + e < p.N ? p.bias[col + e] : 0.0f), p.act);
+                sum[e] = activate(sum[e] + (p.bias && col + e < p.N ? p.bias[col + e] : 0.0f), p.act);
             store_results(p, row, col, sum);
         }
     }

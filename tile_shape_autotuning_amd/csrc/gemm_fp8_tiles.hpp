@@ -277,13 +277,13 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, char* lds, int64_t m0
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = apply_act(acc[i][j][e], TG_ACT_RELU);
+                    acc[i][j][e] = activate(acc[i][j][e], TG_ACT_RELU);
         } else if (p.act == TG_ACT_GELU) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = apply_act(acc[i][j][e], TG_ACT_GELU);
+                    acc[i][j][e] = activate(acc[i][j][e], TG_ACT_GELU);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
