@@ -24,3 +24,12 @@ def test_fast_sums_are_a_part_of_the_type(call):
         assert call(dtype) == N.TG_E_INVAL and "C is bf16" in N.last_error()
     for dtype in (N.BF16, N.BF16_F32OUT):
         assert call(dtype, 0) == N.TG_OK and call(dtype | N.FAST_SUMS, 0) == N.TG_OK
+
+
+def test_gradients_of_a_sum_without_weights_are_refused_by_name():
+    torch = pytest.importorskip("torch")
+    import tile_shape_autotuning_amd as tg
+    x, ids = torch.zeros((2, 64)), torch.zeros((2, 1), dtype=torch.int32)
+    order = tg.MoeOrder(ids, ids[:, 0], torch.zeros(5, dtype=torch.int32))
+    with pytest.raises(TypeError, match="moe_gather"):
+        tg.moe_combine_grad(x, x, order, None)

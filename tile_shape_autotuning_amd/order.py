@@ -149,9 +149,12 @@ def moe_combine_grad(dy, x, order, weights, out=None):
     Returns (dx, dweights): dx[position[t, j]] = weights[t, j] * dy[t], like x
     (rows that no pair has are left as they were in `out`, and hold anything in
     a new tensor); dweights[t, j] = <dy[t], x[position[t, j]]>, float32 [T, k],
-    0 for pairs without a row.
+    0 for pairs without a row.  weights has to be given: without it the gradient
+    of x is moe_gather(dy, order).
     """
     import torch
+    if weights is None:
+        raise TypeError("weights must be given; without weights the gradient of x is moe_gather(dy, order)")
     T, Hy = _rows(dy, "dy")
     n, H = _rows(x, "x")
     if Hy != H or dy.dtype != x.dtype or dy.device != x.device:
