@@ -584,7 +584,8 @@ int tg_fp8_quantize(int64_t count, int64_t R, int64_t K, int block, const void *
  * aligned (NULL where that is 0, as for M <= 64), not shared by calls that may
  * overlap; the size is for the device description in force.  C must not overlap
  * the inputs.  The same call gives the same bits.
- * Limits: M, N <= 2^24, K <= 2^22 (TG_E_UNSUPPORTED).
+ * Limits: M, N <= 2^24, K <= 2^22, and one launch of at most 2^22 workgroups, a
+ * tile of C each, which M * N <= 2^36 always fits (TG_E_UNSUPPORTED).
  */
 int tg_gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
 int tg_gemm_fp8(int64_t M, int64_t N, int64_t K, const tg_f8 *A, const tg_f8 *B, const float *bias, void *C,
@@ -624,7 +625,9 @@ int tg_moe_gather(int64_t T, int k, int64_t rows, const int32_t *position, int64
  * rising; what they name outside [0, rows) is skipped.  Rows outside every
  * expert's are not read, and left as they were in C.  TG_FAST_SUMS may be added to
  * dtype, with effect for more than 32 rows an expert on average.
- * Limits: E <= 1024, rows, N <= 2^24, K <= 2^22 (TG_E_UNSUPPORTED).
+ * Limits: E <= 1024, rows, N <= 2^24, K <= 2^22, and one launch of at most 2^22
+ * workgroups, which (ceil(rows / 16) + min(E, rows)) * ceil(N / 64) <= 2^22 always
+ * fits (TG_E_UNSUPPORTED).
  */
 int tg_moe_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t K, const tg_f8 *A, const tg_f8 *B,
                     const int32_t *offsets, void *C, int dtype);
