@@ -1,7 +1,8 @@
 // Tokens in the order of their experts, and back: the sort of (token, choice)
 // pairs, the copy of rows into that order, the weighted sum that brings them
 // back, and its gradients.  Everything here is bound by memory, but for the
-// sort's latency.  No atomics: the same call gives the same bits.
+// sort's latency.  The same call gives the same bits: the only atomics are counts
+// of pairs in LDS, whole numbers whose order does not matter.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
