@@ -167,3 +167,18 @@ def test_few_rows_have_the_same_bits_with_fast_sums():
         A, B = _random(rng, M, 700, 1)[0], _random(rng, 90, 700, 128)[0]
         for dt in BOTH:
             assert torch.equal(tg.gemm_fp8(A, B, out_dtype=dt), tg.gemm_fp8(A, B, out_dtype=dt, fast_sums=True))
+
+
+@pytest.mark.parametrize("n,N,K", [(7, 150, 1000), (90, 300, 777), (1500, 260, 400)])
+@pytest.mark.parametrize("block", [1, 128])
+def test_sums_of_experts_are_fp32(n, N, K, block):
+    rng = np.random.default_rng(n + K)
+    (A, a, sa), (B, b, sb) = _random(rng, n, K, 1), _random(rng, N, K, block, (3,))
+    ends = np.array([0, n // 2, n // 2 + 1, n], np.int32)
+    C = _np(tg.moe_gemm_fp8(A, B, torch.from_numpy(ends).cuda(), out_dtype=torch.float32))
+    for e in range(3):
+        at = np.s_[ends[e]:ends[e + 1]]
+        left, right = a[at] * np.repeat(sa[at], 128, axis=1), b[e] * np.repeat(sb[e], 128, axis=1)
+        # additions as in _sums; nothing is cut
+        off = (130 + 2 * sa.shape[1]) * 2.0 ** -23 * (np.abs(left) @ np.abs(right).T)
+        assert (np.abs(C[at] - left @ right.T) <= off).all()
