@@ -107,8 +107,9 @@ namespace tg {
 
 // C = act(sums of the S parts of the reduction, in order, + bias): four
 // neighbouring results a thread, all of its loads on their way at once.  Bound by
-// memory: 4 S bytes read a result, once.  (splitk_reduce does the same for other
-// products, whose ReLU makes a NaN 0.)
+// memory, 4 S bytes read a result, once; small results by a launch and one round
+// trip (100 x 4096 in 4 parts and 100 x 1000 in 16: 4 us each).  (splitk_reduce does
+// the same for other products, whose ReLU makes a NaN 0.)
 template <int S>
 __global__ void __launch_bounds__(256) gemm_fp8_parts_kernel(F8Params p)
 {
@@ -173,11 +174,23 @@ static int launch_stream(const F8Params& p, hipStream_t s)
 
 // Panels a workgroup, depth of the ring and waves: where there are many panels
 // several of them share the rows' traffic, where there are few each gets a
-// workgroup, and many waves, to itself (16 x 28672 x 8192: eight panels 44 us, one
-// 64; 1 x 4096 x 4096: one panel 5.6, eight 20).  Experts have about `rows` rows
-// each, often fewer: one or two tiles of 16, and two waves, so that a compute unit
-// holds several workgroups (64 tokens over 64 experts of 2816 x 2048 63 us, with
-// four waves 72; 256 tokens: two tiles 83, one 94).
+// workgroup, and many waves, to itself.  With K = 4096, kernels alone, us:
+//   panels            256    384    512    640    768   1024   1280   1536   1792   2560
+//   16 rows   one     6.8    9.8   10.3   13.7   15.6   19.1   24.8   27.8   32.4   43.7
+//            four    10.9   11.4   11.9   12.6   13.3   15.6   24.4   26.6   28.0   41.2
+//           eight    18.1   18.5   19.0   19.4   19.6   20.2   21.9   24.3   26.5   45.5
+//   32 rows   one     7.9   12.2   12.6   17.1   18.2   23.1   29.2   33.6   39.1   52.9
+//            four    12.9   13.5   14.1   14.8   15.5   17.3   27.7   29.5   31.0   45.2
+//   64 rows   one    10.6   18.6   19.4   27.3   28.1   36.6   45.6   54.1   62.8   88.7
+//            four    19.8   20.3   21.0   21.7   22.5   24.2   33.4   34.5   35.2   51.1
+// so one panel below some 550, and eight for 16 rows from 1200 on: the bounds are
+// two workgroups, and six panels, a compute unit.  (8192 deep, 28672 columns: eight
+// 44 us, one 64.)  Experts have about `rows` rows each, often fewer: one or two tiles
+// of 16, and two waves, so that a compute unit holds several workgroups (64 tokens
+// over 64 experts of 2816 x 2048 63 us, with four waves 72; 256 tokens: two tiles
+// 83, one 94).  One panel and eight waves for few panels of all experts (2048 deep,
+// 8 experts of 16 tokens: 256 panels 5.9 against 11.1 us, 512 8.0 against 11.3, 1024
+// 14.5 against 12.1).
 constexpr int64_t kStreamRows = 64, kStreamExpertRows = 32;
 template <bool BROWS>
 static int stream_by_rows(const F8Params& p, int64_t rows, hipStream_t s)
@@ -208,9 +221,12 @@ struct TileForm {
 };
 
 // Measured (MI355X, 8192 x 8192 by 8192 and by 1024; the deep and the small tiles
-// with 512 and 100 rows): 8192 deep, 256 x 256 has 454 us, 128 x 256 554, 128 x 128
-// 622, 64 x 64 994; with a scale for each row of B 708 (its registers do not
-// suffice), 660, 705, 1,106; exact 1,531, 937, 1,002, 1,425.
+// with 512 and 100 rows).  8192 deep, fast sums: 256 x 256 has 454 us, 128 x 256
+// 554, 128 x 128 622, 64 x 64 994; with a scale for each row of B 708 (its registers
+// do not suffice), 660, 705, 1,106.  Exact, fp32 results: 1,531 (registers again),
+// 937, 1,002, 1,425.  Exact, 4096 x 4096, 128 x 256 to 32 x 64 without parts, bf16:
+// 100 rows 55, 43, 36, 22, 18 us (as planned, in parts, 17), 512 rows 57, 44, 37, 29,
+// 37 (28), 2048 rows 63, 65, 77, 97, 118 (63), 8192 rows 240, 237, 297, 366, 449 (238).
 constexpr float kNever = 1e9f;
 static const TileForm kForms[kTiles] = {{256, 256, 1, 8.7f, {1.64f, kNever, kNever, kNever}},
                                         {128, 256, 1, 5.3f, {1.00f, 1.21f, 1.68f, 1.85f}},
@@ -291,6 +307,8 @@ static int64_t stream_rows(int64_t M, int64_t experts)
 
 static int launch_gemm(F8Params p, bool exact, void* workspace, size_t workspace_bytes, hipStream_t s)
 {
+    // 8192 x 8192 x 8192, 1 to 32 row tiles: 977, 923, 906, 902, 909, 942 us (fast sums
+    // 467, 448, 441, 442, 451, 478); 8192 x 28672 x 4096 1787, 1722, 1708, 1691, 1701, 1761
     p.group_m = 8;
     p.vec_out = p.N % 4 == 0 && (uintptr_t)p.C % (p.out_bf16 ? 8 : 16) == 0;
     p.line_out = p.N % 8 == 0 && (uintptr_t)p.C % 16 == 0;
