@@ -37,8 +37,8 @@ typedef enum {
     TG_E_CACHE = -6         /* tuning-cache file missing, unreadable or malformed */
 } tg_status;
 
-/* input -> output element types; accumulation is always fp32 (TG_FAST_SUMS, which a call on 8-bit matrices may ask for,
- * is the one exception) */
+/* input -> output element types; accumulation is always fp32, but where a
+ * product of 8-bit matrices asks for TG_FAST_SUMS */
 typedef enum {
     TG_F32 = 0,          /* fp32 in, fp32 out */
     TG_BF16 = 1,         /* bf16 in, bf16 out (round to nearest even) */

@@ -117,7 +117,7 @@ def gemm_fp8(A, B, bias=None, act="none", out=None, out_dtype=None, fast_sums=Fa
     columns), block 1 or 128; bias: [N] float32 or None; act: "none" | "relu" |
     "gelu"; out_dtype: torch.bfloat16 (default) or torch.float32.  All sums are
     fp32; fast_sums=True lets the matrix cores' 8-bit form add up the products of
-    more than 64 rows, in up to half the time, which loses small products beside
+    more than 64 rows, at up to twice the rate, which loses small products beside
     large ones (tilegemm.h).  Runs on the current stream and returns C [M, N].
 
     A layer and its gradients, x [T, K], W [N, K], dy [T, N]:
